@@ -417,6 +417,144 @@ ar_status ar_check_noalloc(ar_ctx* ctx, void* const* bufs, int nranks, size_t co
                            ar_dtype dtype, const double* ref, const double* bound,
                            ar_check_result* result);
 
+/* ------------------------------------------------------- training operators
+ *
+ * Operators of the networks whose gradient buckets the collectives above
+ * reduce: layer norm, tokens sorted by expert and back, and distillation from
+ * a teacher's top logits, each with its gradient.  Conventions:
+ *  - Every array is DEVICE memory of the context's device, naturally aligned
+ *    (any element-aligned address is accepted).  Sizes and strides are in
+ *    elements.  Inputs with a stride argument hold row r at r * stride
+ *    (stride >= the row's length); every other array is dense.
+ *  - dtype is AR_FLOAT32 or AR_BFLOAT16.  Statistics, weights of the experts'
+ *    outputs, losses and their gradients are binary32.  All sums are binary32;
+ *    each output is rounded once, to the nearest, ties to even.
+ *  - An output may overlap neither an input nor another output.
+ *  - Every call validates its arguments, enqueues its kernels on the context's
+ *    stream and returns without waiting.  No call allocates device memory:
+ *    scratch is the caller's `workspace` of at least the bytes that the
+ *    operator's *_workspace function tells (16-byte aligned; NULL where that
+ *    is 0), which the call alone uses until its kernels have run.
+ *  - Every call can be captured into a graph, and gives the same bits for the
+ *    same inputs each time: no result depends on the order of atomics.
+ *  - Errors: AR_ERR_INVALID_ARG for a NULL, misaligned, misplaced or
+ *    overlapping array, a size out of range, an unknown dtype or a workspace
+ *    that is too small; AR_ERR_UNSUPPORTED where a limit below is passed;
+ *    AR_ERR_RUNTIME if a launch fails. */
+
+/* Whether the operators' calls check each array with the runtime (device
+ * memory of the context's device, inside its allocation; on by default, as
+ * for bufs above).  enable == 0 leaves that to a caller that knows it already,
+ * as the torch binding does from the tensors themselves: the queries cost a
+ * small call more than its kernel.  Errors: ctx == NULL ->
+ * AR_ERR_INVALID_ARG. */
+ar_status ar_set_operator_checks(ar_ctx* ctx, int enable);
+
+/* Layer norm over rows of `cols` elements (cols > 0):
+ *   mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias
+ * weight and bias: `cols` elements of param_dtype, or NULL (1 and 0).  y has
+ * x's dtype; mean and rstd hold `rows` binary32 values.  rows == 0 is a
+ * successful no-op.  eps >= 0 and finite.  Limit (AR_ERR_UNSUPPORTED):
+ * cols <= 2^28. */
+ar_status ar_layer_norm(ar_ctx* ctx, const void* x, size_t x_stride, const void* weight,
+                        const void* bias, ar_dtype param_dtype, void* y, float* mean, float* rstd,
+                        size_t rows, size_t cols, ar_dtype dtype, float eps);
+
+/* Its gradient, from what the forward pass left: with g = dy * weight and
+ * xh = (x - mean) * rstd,
+ *   dx = rstd * (g - sum(g) / cols - xh * sum(g * xh) / cols)
+ *   dweight = sum over rows of dy * xh, dbias = sum over rows of dy
+ * dweight and dbias have param_dtype and may each be NULL (not wanted);
+ * weight NULL means 1.  With rows == 0 they are zeros. */
+ar_status ar_layer_norm_backward(ar_ctx* ctx, const void* dy, size_t dy_stride, const void* x,
+                                 size_t x_stride, const float* mean, const float* rstd,
+                                 const void* weight, ar_dtype param_dtype, void* dx, void* dweight,
+                                 void* dbias, size_t rows, size_t cols, ar_dtype dtype,
+                                 void* workspace, size_t workspace_bytes);
+ar_status ar_layer_norm_backward_workspace(size_t rows, size_t cols, ar_dtype dtype,
+                                           size_t* bytes);
+
+/* Tokens sorted by expert.  ids holds tokens x topk experts (index_bytes 4:
+ * int32, 8: int64); a value outside [0, experts) means no expert.  Slot
+ * i = t * topk + k is token t's k-th choice.  The slots are sorted by expert,
+ * stably, those without one last:
+ *   dest[i]     the sorted row of slot i
+ *   slot[j]     the slot of sorted row j
+ *   offsets[e]  the first row of expert e; offsets[experts] = rows in use
+ *   rows[j]     = x[slot[j] / topk] for j < offsets[experts], zeros beyond
+ * dest and slot: int32, tokens * topk; offsets: int32, experts + 1; rows:
+ * tokens * topk rows of `hidden` elements.  Limits (AR_ERR_UNSUPPORTED):
+ * experts <= AR_MAX_EXPERTS, tokens * topk <= 2^31 - 1.  topk, experts and
+ * hidden > 0.  With tokens == 0 only offsets (zeros) is written. */
+#define AR_MAX_EXPERTS 1024
+ar_status ar_expert_dispatch(ar_ctx* ctx, const void* x, size_t x_stride, const void* ids,
+                             int index_bytes, size_t tokens, int topk, int experts, size_t hidden,
+                             ar_dtype dtype, void* rows, int* dest, int* slot, int* offsets,
+                             void* workspace, size_t workspace_bytes);
+ar_status ar_expert_dispatch_workspace(size_t tokens, int topk, int experts, size_t* bytes);
+
+/* The gradient of x: dx[t] = sum over k of drows[dest[t,k]], over the slots
+ * with an expert. */
+ar_status ar_expert_dispatch_backward(ar_ctx* ctx, const void* drows, const int* dest,
+                                      const int* offsets, size_t tokens, int topk, int experts,
+                                      size_t hidden, ar_dtype dtype, void* dx);
+
+/* The way back: y[t] = sum over k of weights[t,k] * rows[dest[t,k]], in the
+ * order of k, over the slots with an expert (dest < offsets[experts]); what
+ * the other rows and weights hold does not matter.  weights: binary32,
+ * tokens x topk.  A dest outside [0, tokens * topk) counts as no expert. */
+ar_status ar_expert_combine(ar_ctx* ctx, const void* rows, const float* weights, const int* dest,
+                            const int* offsets, size_t tokens, int topk, int experts,
+                            size_t hidden, ar_dtype dtype, void* y);
+
+/* Its gradients: drows[dest[t,k]] = weights[t,k] * dy[t] (zeros in the rows
+ * without an expert), dweights[t,k] = sum(rows[dest[t,k]] * dy[t]) (0 for a
+ * slot without an expert).  drows has dtype, dweights is binary32. */
+ar_status ar_expert_combine_backward(ar_ctx* ctx, const void* dy, size_t dy_stride,
+                                     const void* rows, const float* weights, const int* dest,
+                                     const int* offsets, size_t tokens, int topk, int experts,
+                                     size_t hidden, ar_dtype dtype, void* drows, float* dweights);
+
+/* Distillation from a teacher's top logits.  Row r holds the student's logits
+ * over `vocab` places (row r at r * logits_stride) and the teacher's logits
+ * teacher[r][0..top) at the places indices[r][0..top) (index_bytes 4: int32,
+ * 8: int64); an index outside [0, vocab) leaves its entry out.  With the
+ * temperature T > 0:
+ *   p = softmax(teacher / T) over the entries kept
+ *   q = softmax(logits / T), lse = log(sum(exp(logits / T)))
+ *   loss = T^2 * sum over entries of p * (log p - log q at their places)
+ * An entry with p == 0 adds nothing; a place named twice counts twice; a row
+ * that keeps no entry (or whose kept teacher logits are all -inf) has loss 0.
+ * loss and lse: binary32, rows.  teacher has the logits' dtype.  Limits
+ * (AR_ERR_UNSUPPORTED): top <= AR_DISTILL_MAX_TOP, vocab <= 2^31 - 1.
+ * vocab and top > 0; rows == 0 is a successful no-op. */
+#define AR_DISTILL_MAX_TOP 1024
+ar_status ar_distill_loss(ar_ctx* ctx, const void* logits, size_t logits_stride,
+                          const void* indices, int index_bytes, const void* teacher, size_t rows,
+                          size_t vocab, size_t top, ar_dtype dtype, float temperature, float* loss,
+                          float* lse, void* workspace, size_t workspace_bytes);
+
+/* Its gradient, with dloss (binary32, rows) and the forward pass's lse:
+ *   dlogits = dloss * T * (q - p at the entries' places)
+ * and zeros in a row whose loss is 0 for want of a teacher, whatever its
+ * logits hold.  dlogits: dense, rows x vocab, of the logits' dtype. */
+ar_status ar_distill_backward(ar_ctx* ctx, const float* dloss, const void* logits,
+                              size_t logits_stride, const void* indices, int index_bytes,
+                              const void* teacher, const float* lse, size_t rows, size_t vocab,
+                              size_t top, ar_dtype dtype, float temperature, void* dlogits);
+
+/* Loss and gradient at once, for a caller that knows each row's share dloss
+ * beforehand (a mean over the batch).  The workspace functions tell what
+ * ar_distill_loss (gradient == 0) and ar_distill_step (gradient != 0) take. */
+ar_status ar_distill_step(ar_ctx* ctx, const float* dloss, const void* logits,
+                          size_t logits_stride, const void* indices, int index_bytes,
+                          const void* teacher, size_t rows, size_t vocab, size_t top,
+                          ar_dtype dtype, float temperature, float* loss, void* dlogits,
+                          void* workspace, size_t workspace_bytes);
+ar_status ar_distill_workspace(size_t rows, size_t vocab, ar_dtype dtype, int gradient,
+                               size_t* bytes);
+
 /* Static description of a status code (never NULL). */
 const char* ar_status_string(ar_status s);
 

@@ -28,9 +28,25 @@ __all__ = [
     "ring_ag_step", "tree_step", "hd_rs_step", "hd_ag_step", "dtree_step", "copy_", "stream_",
     "check", "chunk_range", "bind", "bind_stream", "stream_timeline",
     "context", "LIB_PATH", "predict_us", "auto_algo", "set_graphs", "set_residency_caps",
+    "ExpertPlan", "layer_norm", "layer_norm_backward", "expert_dispatch",
+    "expert_dispatch_backward", "expert_combine", "expert_combine_backward", "distill_loss",
+    "distill_backward", "distill_step",
 ]
 
+_OPERATORS = frozenset(__all__[__all__.index("ExpertPlan"):])
+
 _ctx: dict = {}
+
+
+def __getattr__(name):
+    # the training operators need torch when they are imported, the
+    # collectives' host-only functions do not
+    if name in _OPERATORS:
+        from . import operators
+        for n in _OPERATORS:
+            globals()[n] = getattr(operators, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

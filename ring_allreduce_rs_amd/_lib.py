@@ -15,6 +15,8 @@ LIB_PATH = os.path.join(_PKG, "libar.so")
 
 AR_MAX_RANKS = 64
 AR_GRAPHS_MAX_BYTES_DEFAULT = 8 << 20
+AR_MAX_EXPERTS = 1024
+AR_DISTILL_MAX_TOP = 1024
 
 AR_OK = 0
 AR_ERR_INVALID_ARG = 1
@@ -35,6 +37,10 @@ EXPORTS = (
     "ar_reduce_scatter", "ar_allgather", "ar_ring_rs_step", "ar_ring_ag_step", "ar_tree_step",
     "ar_hd_rs_step", "ar_hd_ag_step", "ar_dtree_step", "ar_chunk_range", "ar_predict_us",
     "ar_auto_algo", "ar_copy", "ar_stream", "ar_stream_timeline", "ar_check", "ar_check_noalloc",
+    "ar_set_operator_checks", "ar_layer_norm", "ar_layer_norm_backward",
+    "ar_layer_norm_backward_workspace", "ar_expert_dispatch", "ar_expert_dispatch_workspace",
+    "ar_expert_dispatch_backward", "ar_expert_combine", "ar_expert_combine_backward",
+    "ar_distill_loss", "ar_distill_backward", "ar_distill_step", "ar_distill_workspace",
     "ar_status_string",
     "ar_last_error", "ar_destroy",
 )
@@ -64,6 +70,7 @@ def _load() -> ctypes.CDLL:
             "(or __graft_entry__.build()) first")
     lib = ctypes.CDLL(LIB_PATH)
     vp, sz, i, cp = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_char_p
+    f, psz = ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "ar_create": ([ctypes.POINTER(vp), i, vp], i),
@@ -91,6 +98,20 @@ def _load() -> ctypes.CDLL:
                                 ctypes.POINTER(ctypes.c_uint)], i),
         "ar_check": ([vp, pp, i, sz, i, vp, vp, vp], i),
         "ar_check_noalloc": ([vp, pp, i, sz, i, vp, vp, vp], i),
+        "ar_set_operator_checks": ([vp, i], i),
+        "ar_layer_norm": ([vp, vp, sz, vp, vp, i, vp, vp, vp, sz, sz, i, f], i),
+        "ar_layer_norm_backward": ([vp, vp, sz, vp, sz, vp, vp, vp, i, vp, vp, vp, sz, sz, i,
+                                    vp, sz], i),
+        "ar_layer_norm_backward_workspace": ([sz, sz, i, psz], i),
+        "ar_expert_dispatch": ([vp, vp, sz, vp, i, sz, i, i, sz, i, vp, vp, vp, vp, vp, sz], i),
+        "ar_expert_dispatch_workspace": ([sz, i, i, psz], i),
+        "ar_expert_dispatch_backward": ([vp, vp, vp, vp, sz, i, i, sz, i, vp], i),
+        "ar_expert_combine": ([vp, vp, vp, vp, vp, sz, i, i, sz, i, vp], i),
+        "ar_expert_combine_backward": ([vp, vp, sz, vp, vp, vp, vp, sz, i, i, sz, i, vp, vp], i),
+        "ar_distill_loss": ([vp, vp, sz, vp, i, vp, sz, sz, sz, i, f, vp, vp, vp, sz], i),
+        "ar_distill_backward": ([vp, vp, vp, sz, vp, i, vp, vp, sz, sz, sz, i, f, vp], i),
+        "ar_distill_step": ([vp, vp, vp, sz, vp, i, vp, sz, sz, sz, i, f, vp, vp, vp, sz], i),
+        "ar_distill_workspace": ([sz, sz, i, i, psz], i),
         "ar_status_string": ([i], cp),
         "ar_last_error": ([vp], cp),
         "ar_destroy": ([vp], i),
@@ -193,6 +214,18 @@ class Context:
         (ar_set_residency_caps); results are the same bits either way."""
         self._check(lib.ar_set_residency_caps(self._h, 1 if enable else 0),
                     "ar_set_residency_caps")
+
+    def set_operator_checks(self, enable: bool) -> None:
+        """Whether the operators' calls ask the runtime about each array
+        (ar_set_operator_checks)."""
+        self._check(lib.ar_set_operator_checks(self._h, 1 if enable else 0),
+                    "ar_set_operator_checks")
+
+    def call(self, fn, *args) -> None:
+        """An operator's entry point of `lib` with its arguments after ctx."""
+        st = fn(self._h, *args)
+        if st != AR_OK:
+            raise ArError(st, fn.__name__, self.last_error())
 
     def last_error(self) -> str:
         return lib.ar_last_error(self._h).decode()

@@ -1,0 +1,360 @@
+// distill.hip -- distillation from a teacher's top logits, forward and backward.
+//
+// A row holds the student's logits z over the vocabulary, and the teacher's
+// logits t at `top` places i_1 .. i_top.  With the temperature T:
+//   p = softmax(t / T) over the entries kept (0 <= i_j < vocab)
+//   q = softmax(z / T) over the vocabulary,  lse = log sum exp(z / T)
+//   loss = T^2 sum_j p_j (log p_j - log q_{i_j})
+//   d loss / d z_v = T (q_v - sum_{j: i_j = v} p_j)
+// An entry with p_j = 0 adds nothing.  A row without a kept entry (or whose
+// teacher logits are all -inf) has loss 0 and gradient 0, whatever z holds.
+//
+// All sums are fp32 and are split the same way at every call, so results
+// repeat bit for bit.  The traffic is the logits and their gradient; the
+// teacher's entries are staged in LDS.
+#include "ops.h"
+#include "ops_device.h"
+
+namespace arlib {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxTop = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int IB>
+__device__ __forceinline__ int place_of(const void* indices, size_t j, size_t vocab) {
+    if constexpr (IB == 8) {
+        const int64_t v = static_cast<const int64_t*>(indices)[j];
+        return v >= 0 && v < (int64_t)vocab ? (int)v : -1;
+    } else {
+        const int32_t v = static_cast<const int32_t*>(indices)[j];
+        return v >= 0 && (size_t)v < vocab ? v : -1;
+    }
+}
+
+// The teacher of one row in LDS: places (-1: left out) and probabilities.
+struct Teacher {
+    int at[kMaxTop];
+    float p[kMaxTop];
+    float red[2][16];
+};
+
+template <int W>
+__device__ __forceinline__ float block_max(float v, float* lds) {
+    v = wave_max(v);
+    if constexpr (W == 1) return v;
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float t = lds[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) t = fmaxf(t, lds[w]);
+    return t;
+}
+
+// Fills th for row r; returns whether the row has a teacher.  *zmax and *logs
+// are what log p_j = t_j / T - zmax - logs takes.  All threads call it.
+template <int EB, int IB, int W>
+__device__ bool load_teacher(const DistillArgs& a, size_t r, Teacher& th, float* zmax,
+                             float* logs) {
+    constexpr int NT = W * 64;
+    const char* t = static_cast<const char*>(a.teacher) + r * a.top * EB;
+    float m = -INFINITY;
+    for (int j = threadIdx.x; j < (int)a.top; j += NT) {
+        const int at = place_of<IB>(a.indices, r * a.top + j, a.vocab);
+        const float z = at >= 0 ? Vec<EB>::ld1(t + (size_t)j * EB) / a.temperature : -INFINITY;
+        th.at[j] = at;
+        th.p[j] = z;
+        m = z != z ? z : fmaxf(m, z);   // (a NaN reaches the sum below by itself)
+    }
+    m = block_max<W>(m == m ? m : -INFINITY, th.red[0]);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f;
+    for (int j = threadIdx.x; j < (int)a.top; j += NT) {
+        const float e = expf(th.p[j] - base);
+        th.p[j] = e;
+        s += e;
+    }
+    s = block_sum<W>(s, th.red[1]);
+    *zmax = base;
+    *logs = logf(s);
+    const float inv = 1.0f / s;
+    if (!(s == 0.0f))
+        for (int j = threadIdx.x; j < (int)a.top; j += NT) th.p[j] *= inv;
+    __syncthreads();
+    return !(s == 0.0f);
+}
+
+// The row's loss, on every thread.
+template <int EB, int IB, int W>
+__device__ float row_loss(const DistillArgs& a, size_t r, Teacher& th, float zmax, float logs,
+                          float lse) {
+    const char* t = static_cast<const char*>(a.teacher) + r * a.top * EB;
+    const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
+    float s = 0.0f;
+    for (int j = threadIdx.x; j < (int)a.top; j += W * 64) {
+        const float p = th.p[j];
+        if (th.at[j] < 0 || p == 0.0f) continue;
+        const float logp = Vec<EB>::ld1(t + (size_t)j * EB) / a.temperature - zmax - logs;
+        const float logq = Vec<EB>::ld1(z + (size_t)th.at[j] * EB) / a.temperature - lse;
+        s = __builtin_fmaf(p, logp - logq, s);
+    }
+    __syncthreads();   // th.red is free again
+    return block_sum<W>(s, th.red[0]) * (a.temperature * a.temperature);
+}
+
+// Running maximum and sum of exp((z - m) / T), c = log2(e) / T.
+struct Soft {
+    float m, s;
+};
+__device__ __forceinline__ Soft soft_zero() { return {-INFINITY, 0.0f}; }
+// What the sum is relative to: an infinite maximum is left out, so that a row
+// of -inf sums to 0 and a +inf makes the sum (and lse) infinite.
+__device__ __forceinline__ float soft_base(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
+// The base that a sum of this maximum has, seen from another: -inf for an
+// empty one, so that its 0 stays 0.
+__device__ __forceinline__ float soft_from(float m) { return m < INFINITY ? m : 0.0f; }
+__device__ __forceinline__ float soft_lse(Soft v, float temperature) {
+    return soft_base(v.m) / temperature + logf(v.s);
+}
+__device__ __forceinline__ Soft soft_join(Soft a, Soft b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    const float base = soft_base(m);
+    // (a NaN in either sum stays in the sum)
+    return {m, a.s * exp2_fast((soft_from(a.m) - base) * c) +
+                   b.s * exp2_fast((soft_from(b.m) - base) * c)};
+}
+template <int E>
+__device__ __forceinline__ void soft_add(Soft& a, const float (&v)[E], float c) {
+    float m = a.m;
+#pragma unroll
+    for (int j = 0; j < E; ++j) m = fmaxf(m, v[j]);
+    const float base = soft_base(m);
+    float s = a.s * exp2_fast((soft_from(a.m) - base) * c);
+#pragma unroll
+    for (int j = 0; j < E; ++j) s += exp2_fast((v[j] - base) * c);
+    a.m = m;
+    a.s = s;
+}
+template <int W>
+__device__ __forceinline__ Soft block_soft(Soft v, float c, Soft* lds) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const Soft o = {__shfl_xor(v.m, d, 64), __shfl_xor(v.s, d, 64)};
+        v = soft_join(v, o, c);
+    }
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v = soft_join(v, lds[w], c);
+    return v;
+}
+
+// Column chunks of a row: chunk elements each (a multiple of a unit), `parts`
+// of them.
+template <int EB>
+__global__ __launch_bounds__(kThreads) void k_distill_part(const DistillArgs a, size_t parts,
+                                                           size_t chunk) {
+    constexpr int E = Vec<EB>::E;
+    __shared__ Soft lds[kWaves];
+    const float c = kLog2e / a.temperature;
+    for (size_t task = blockIdx.x; task < a.rows * parts; task += gridDim.x) {
+        const size_t r = task / parts, lo = (task % parts) * chunk;
+        const size_t hi = lo + chunk < a.vocab ? lo + chunk : a.vocab;
+        const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
+        const uint32_t ninf = EB == 2 ? 0xff80ff80u : 0xff800000u;
+        Soft acc = soft_zero();
+        for (size_t i = lo + (size_t)threadIdx.x * E; i < hi; i += (size_t)kThreads * E) {
+            float v[E];
+            // (a tail element's bits sit in the low half of `fill`)
+            Vec<EB>::unpack(ld_unit_of<EB>(z, i, hi, ninf), v);
+            soft_add<E>(acc, v, c);
+        }
+        acc = block_soft<kWaves>(acc, c, lds);
+        if (threadIdx.x == 0) {
+            a.part[2 * task] = acc.m;
+            a.part[2 * task + 1] = acc.s;
+        }
+        __syncthreads();
+    }
+}
+
+// The row's maximum and sum from its parts, on every thread.
+__device__ __forceinline__ Soft fold_parts(const DistillArgs& a, size_t r, size_t parts, float c) {
+    Soft v = soft_zero();
+    for (size_t k = threadIdx.x & 63; k < parts; k += 64)
+        v = soft_join(v, Soft{a.part[2 * (r * parts + k)], a.part[2 * (r * parts + k) + 1]}, c);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const Soft o = {__shfl_xor(v.m, d, 64), __shfl_xor(v.s, d, 64)};
+        v = soft_join(v, o, c);
+    }
+    return v;
+}
+
+// Loss and lse of each row from its parts.
+template <int EB, int IB>
+__global__ __launch_bounds__(kThreads) void k_distill_loss(const DistillArgs a, size_t parts) {
+    __shared__ Teacher th;
+    const float c = kLog2e / a.temperature;
+    for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const Soft v = fold_parts(a, r, parts, c);
+        const float lse = soft_lse(v, a.temperature);
+        float zmax, logs;
+        const bool some = load_teacher<EB, IB, kWaves>(a, r, th, &zmax, &logs);
+        float loss = row_loss<EB, IB, kWaves>(a, r, th, zmax, logs, lse);
+        if (threadIdx.x == 0) {
+            a.loss[r] = some ? loss : 0.0f;
+            if (a.lse) a.lse[r] = lse;
+        }
+        __syncthreads();
+    }
+}
+
+// The gradient of one chunk of a row.  q from the parts (PARTS) or from lse_in.
+// The kept entries are written after the rest of the chunk, each place by the
+// first entry that names it with the sum of its duplicates.
+template <int EB, int IB, bool PARTS>
+__global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, size_t parts,
+                                                           size_t chunk, size_t soft_parts) {
+    constexpr int E = Vec<EB>::E;
+    __shared__ Teacher th;
+    const float c = kLog2e / a.temperature;
+    for (size_t task = blockIdx.x; task < a.rows * parts; task += gridDim.x) {
+        const size_t r = task / parts, lo = (task % parts) * chunk;
+        const size_t hi = lo + chunk < a.vocab ? lo + chunk : a.vocab;
+        const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
+        char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;
+        float zmax, logs;
+        const bool some = load_teacher<EB, IB, kWaves>(a, r, th, &zmax, &logs);
+        const float scale = a.dloss[r] * a.temperature;
+        float base = 0.0f, lse = 0.0f, inv = 1.0f;
+        if constexpr (PARTS) {
+            const Soft v = fold_parts(a, r, soft_parts, c);
+            base = soft_base(v.m);
+            inv = 1.0f / v.s;
+            if (lo == 0) {   // (uniform over the block)
+                const float loss =
+                    row_loss<EB, IB, kWaves>(a, r, th, zmax, logs, soft_lse(v, a.temperature));
+                if (threadIdx.x == 0) a.loss[r] = some ? loss : 0.0f;
+            }
+        } else {
+            lse = a.lse_in[r];
+        }
+        const auto prob = [&](float v) -> float {
+            if constexpr (PARTS) return exp2_fast((v - base) * c) * inv;
+            else return expf(v / a.temperature - lse);
+        };
+        for (size_t i = lo + (size_t)threadIdx.x * E; i < hi; i += (size_t)kThreads * E) {
+            float v[E];
+            Vec<EB>::unpack(ld_unit_of<EB>(z, i, hi, 0u), v);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = some ? prob(v[j]) * scale : 0.0f;
+            st_unit_of<EB>(dz, i, hi, Vec<EB>::pack(v));
+        }
+        __syncthreads();
+        if (some)
+            for (int j = threadIdx.x; j < (int)a.top; j += kThreads) {
+                const int at = th.at[j];
+                if (at < 0 || (size_t)at < lo || (size_t)at >= hi) continue;
+                float p = 0.0f;
+                bool mine = true;
+                for (int k = 0; k < (int)a.top; ++k)
+                    if (th.at[k] == at) {
+                        mine &= k >= j;
+                        p += th.p[k];
+                    }
+                if (mine) {
+                    const float q = prob(Vec<EB>::ld1(z + (size_t)at * EB));
+                    Vec<EB>::st1(dz + (size_t)at * EB, (q - p) * scale);
+                }
+            }
+        __syncthreads();
+    }
+}
+
+// The split of a row into chunks: kChunkBytes, more blocks for few rows.
+struct Split {
+    size_t parts, chunk;
+};
+Split split_of(size_t rows, size_t vocab, int eb) {
+    const size_t e = 16 / eb, unit = (size_t)kThreads * e;   // one unit per thread
+    size_t parts = (vocab + 16 * unit - 1) / (16 * unit);
+    const size_t most = (vocab + unit - 1) / unit;
+    while (rows * parts < 512 && parts < most) parts = parts * 2 < most ? parts * 2 : most;
+    size_t chunk = (vocab + parts - 1) / parts;
+    chunk = (chunk + e - 1) / e * e;
+    return {(vocab + chunk - 1) / chunk, chunk};
+}
+
+unsigned grid_of(size_t tasks) {
+    constexpr size_t kMost = size_t(1) << 22;
+    return (unsigned)(tasks < kMost ? tasks : kMost);
+}
+
+#define DISTILL_BY_TYPE(CALL)                     \
+    do {                                          \
+        if (a.eb == 2 && a.ib == 4) { CALL(2, 4); } \
+        else if (a.eb == 2) { CALL(2, 8); }       \
+        else if (a.ib == 4) { CALL(4, 4); }       \
+        else { CALL(4, 8); }                      \
+    } while (0)
+
+hipError_t launch_part(const DistillArgs& a, Split sp, hipStream_t s) {
+    const dim3 grid(grid_of(a.rows * sp.parts)), block(kThreads);
+    if (a.eb == 2) hipLaunchKernelGGL(k_distill_part<2>, grid, block, 0, s, a, sp.parts, sp.chunk);
+    else hipLaunchKernelGGL(k_distill_part<4>, grid, block, 0, s, a, sp.parts, sp.chunk);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t distill_work_floats(size_t rows, size_t vocab, int eb, bool step) {
+    (void)step;
+    if (rows == 0) return 0;
+    return 2 * rows * split_of(rows, vocab, eb).parts;
+}
+
+hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s) {
+    if (a.rows == 0) return hipSuccess;
+    const Split sp = split_of(a.rows, a.vocab, a.eb);
+    const hipError_t e = launch_part(a, sp, s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(grid_of(a.rows)), block(kThreads);
+#define CALL(EB, IB) hipLaunchKernelGGL((k_distill_loss<EB, IB>), grid, block, 0, s, a, sp.parts)
+    DISTILL_BY_TYPE(CALL);
+#undef CALL
+    return hipGetLastError();
+}
+
+hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s) {
+    if (a.rows == 0) return hipSuccess;
+    const Split sp = split_of(a.rows, a.vocab, a.eb);
+    const dim3 grid(grid_of(a.rows * sp.parts)), block(kThreads);
+#define CALL(EB, IB) \
+    hipLaunchKernelGGL((k_distill_grad<EB, IB, false>), grid, block, 0, s, a, sp.parts, sp.chunk, \
+                       size_t(0))
+    DISTILL_BY_TYPE(CALL);
+#undef CALL
+    return hipGetLastError();
+}
+
+hipError_t launch_distill_step(const DistillArgs& a, hipStream_t s) {
+    if (a.rows == 0) return hipSuccess;
+    const Split sp = split_of(a.rows, a.vocab, a.eb);
+    const hipError_t e = launch_part(a, sp, s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(grid_of(a.rows * sp.parts)), block(kThreads);
+#define CALL(EB, IB) \
+    hipLaunchKernelGGL((k_distill_grad<EB, IB, true>), grid, block, 0, s, a, sp.parts, sp.chunk, \
+                       sp.parts)
+    DISTILL_BY_TYPE(CALL);
+#undef CALL
+    return hipGetLastError();
+}
+
+}  // namespace arlib
