@@ -1,4 +1,5 @@
-"""Build libar.so (HIP kernels + C ABI) in-tree for gfx950.
+"""Build libar.so (HIP kernels + C ABI) and _torch_ops.so (the operators'
+binding to torch tensors) in-tree for gfx950.
 
 Run ``python ring_allreduce_rs_amd/_build.py`` or ``__graft_entry__.build()``
 (the script does not import the package, which needs the library).
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -19,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libar.so")
+TORCH_OPS = os.path.join(PKG, "_torch_ops.so")
 
 # the fused kernels are instantiated per element type so the (slowest) device
 # compilations run side by side
@@ -50,13 +53,17 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libar.so)")
 
 
+def rocm_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+
+
 def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed with exit code {res.returncode}: {' '.join(cmd[-3:])}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed with exit code {res.returncode}: {' '.join(cmd[-3:])}")
     if verbose and res.stderr.strip():
         sys.stderr.write(res.stderr)
 
@@ -76,7 +83,28 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         tmp = LIB + ".tmp"
         _run([hipcc(), *FLAGS, *(extra_flags or []), "-shared", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
+    build_torch_ops(verbose)
     return LIB
+
+
+def build_torch_ops(verbose: bool = False) -> str:
+    """Compile the torch binding of the operators against libar.so and the
+    installed torch (host code only); returns its path."""
+    import torch
+    from torch.utils import cpp_extension
+
+    dirs = [*cpp_extension.include_paths(), os.path.join(rocm_home(), "include"),
+            sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[a for d in dirs for a in ("-isystem", d)], "-I", INCLUDE,
+           os.path.join(CSRC, "torch_ops.cpp"), "-o", TORCH_OPS + ".tmp",
+           *["-L" + p for p in cpp_extension.library_paths()], "-L" + PKG, "-l:libar.so", "-lc10",
+           "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    _run(cmd, verbose)
+    os.replace(TORCH_OPS + ".tmp", TORCH_OPS)
+    return TORCH_OPS
 
 
 if __name__ == "__main__":

@@ -12,6 +12,7 @@ import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libar.so")
+TORCH_OPS_PATH = os.path.join(_PKG, "_torch_ops.so")
 
 AR_MAX_RANKS = 64
 AR_GRAPHS_MAX_BYTES_DEFAULT = 8 << 20
@@ -214,18 +215,6 @@ class Context:
         (ar_set_residency_caps); results are the same bits either way."""
         self._check(lib.ar_set_residency_caps(self._h, 1 if enable else 0),
                     "ar_set_residency_caps")
-
-    def set_operator_checks(self, enable: bool) -> None:
-        """Whether the operators' calls ask the runtime about each array
-        (ar_set_operator_checks)."""
-        self._check(lib.ar_set_operator_checks(self._h, 1 if enable else 0),
-                    "ar_set_operator_checks")
-
-    def call(self, fn, *args) -> None:
-        """An operator's entry point of `lib` with its arguments after ctx."""
-        st = fn(self._h, *args)
-        if st != AR_OK:
-            raise ArError(st, fn.__name__, self.last_error())
 
     def last_error(self) -> str:
         return lib.ar_last_error(self._h).decode()

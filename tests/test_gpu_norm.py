@@ -202,6 +202,22 @@ def test_captured_graph():
         torch.cuda.synchronize()
 
 
+def test_views_with_even_rows():
+    """Leading dimensions that one stride walks, and those that none does."""
+    x = torch.randn(6, 40, device="cuda")
+    check_forward(x[:, :7], None, None)
+    check_forward(x[::2], None, None)
+    check_forward(x[1], None, None)
+    check_forward(x.view(2, 3, 40)[:, :, 3:9], None, None)
+    check_forward(x.view(2, 3, 40)[1:, :, 1:], None, None)
+    check_forward(x.view(6, 1, 40)[:, :, :5], None, None)
+    check_forward(x[:, :1].t().contiguous().t(), None, None)
+    for bad in (x.t(), x[:, ::2], x[:1].expand(6, 40), x.view(2, 3, 40).transpose(0, 1),
+                x.as_strided((3, 8), (4, 1)), x.view(2, 3, 40)[:, :2], x[0, 0]):
+        with pytest.raises(ValueError):
+            ar.layer_norm(bad)
+
+
 def test_refusals():
     x = torch.randn(4, 32, device="cuda")
     w = torch.ones(32, device="cuda")

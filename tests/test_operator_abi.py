@@ -6,6 +6,7 @@ refusals of the torch binding that need no GPU."""
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -60,15 +61,14 @@ def test_tensors_off_the_gpu_are_refused():
             call()
 
 
-def test_row_strides():
-    from ring_allreduce_rs_amd.operators import _row_stride
-    x = torch.zeros(6, 40)
-    assert _row_stride(x, "x") == 40
-    assert _row_stride(x[:, :7], "x") == 40
-    assert _row_stride(x[::2], "x") == 80
-    assert _row_stride(x[0], "x") == 40
-    assert _row_stride(x.view(2, 3, 40)[:, :, 3:9], "x") == 40
-    for bad in (x.t(), x[:, ::2], x[:1].expand(6, 40), x.view(2, 3, 40).transpose(0, 1),
-                x.as_strided((3, 8), (4, 1)), torch.zeros(())):
-        with pytest.raises(ValueError):
-            _row_stride(bad, "x")
+def test_the_binding_says_what_to_build(tmp_path):
+    # a copy without _torch_ops.so must raise when an operator is asked for
+    pkg = tmp_path / "ring_allreduce_rs_amd"
+    shutil.copytree(os.path.join(ROOT, "ring_allreduce_rs_amd"), pkg,
+                    ignore=shutil.ignore_patterns("_torch_ops*", "__pycache__", "csrc"))
+    code = ("import sys; sys.path.insert(0, %r)\n"
+            "import ring_allreduce_rs_amd as ar\n"
+            "try:\n ar.layer_norm\nexcept ImportError as e:\n print('RAISED', e)\n"
+            % str(tmp_path))
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert "RAISED" in out.stdout and "_build.py" in out.stdout, out.stdout + out.stderr
