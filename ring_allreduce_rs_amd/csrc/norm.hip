@@ -18,6 +18,207 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kNormWaves = kNormThreads / 64;
 
+__device__ __forceinline__ void st_param(void* base, int pb, size_t i, float v) {
+    if (pb == 4) Vec<4>::st1(static_cast<char*>(base) + i * 4, v);
+    else Vec<2>::st1(static_cast<char*>(base) + i * 2, v);
+}
+
+// Rows that a block holds in registers: NT threads with UPT units each, R rows
+// at a time, so that a block has R rows of loads in flight and one barrier
+// serves R sums.  The parameters stay in registers from row to row.  Rows past
+// the last are loaded as the last one again and left out of sums and stores.
+template <int EB, int NT, int UPT, int R, bool RAGGED>
+__global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
+    constexpr int E = Vec<EB>::E, W = NT / 64;
+    __shared__ float lds[2][W * R];
+    const float n = (float)a.cols;
+    Place at[UPT];
+    float w[UPT][E], b[UPT][E];
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
+        ld_params<E>(a.weight, a.pb, at[u].at, a.cols, 1.0f, w[u]);
+        ld_params<E>(a.bias, a.pb, at[u].at, a.cols, 0.0f, b[u]);
+    }
+    for (size_t r0 = (size_t)blockIdx.x * R; r0 < a.rows; r0 += (size_t)gridDim.x * R) {
+        u32x4 raw[R][UPT];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const size_t r = r0 + k < a.rows ? r0 + k : a.rows - 1;
+            const char* x = static_cast<const char*>(a.x) + r * a.xstride * EB;
+#pragma unroll
+            for (int u = 0; u < UPT; ++u)
+                raw[k][u] = ld_unit<EB, true>(x + offset_here(at[u].at * EB));
+        }
+        float mean[R], s[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                if (at[u].skip) raw[k][u] = drop_first<EB, RAGGED>(raw[k][u], at[u].skip);
+                float v[E];
+                Vec<EB>::unpack(raw[k][u], v);
+#pragma unroll
+                for (int j = 0; j < E; ++j) mean[k] += v[j];
+            }
+        }
+        block_sums<W, R>(mean, lds[0]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] /= n;
+            s[k] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                float v[E];
+                refresh(raw[k][u]);
+                Vec<EB>::unpack(raw[k][u], v);
+                if (at[u].skip) {   // the dropped elements read as the mean
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = !RAGGED || j < at[u].skip ? mean[k] : v[j];
+                }
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float d = v[j] - mean[k];
+                    s[k] = __builtin_fmaf(d, d, s[k]);
+                }
+            }
+        }
+        block_sums<W, R>(s, lds[1]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k >= a.rows) break;
+            const float rstd = 1.0f / sqrtf(s[k] / n + a.eps);
+            char* y = static_cast<char*>(a.y) + (r0 + k) * a.cols * EB;
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                float v[E];
+                refresh(raw[k][u]);
+                Vec<EB>::unpack(raw[k][u], v);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    v[j] = __builtin_fmaf((v[j] - mean[k]) * rstd, w[u][j], b[u][j]);
+                st_place<EB, RAGGED, true>(y, at[u], Vec<EB>::pack(v));
+            }
+            if (threadIdx.x == 0) {
+                a.mean[r0 + k] = mean[k];
+                a.rstd[r0 + k] = rstd;
+            }
+        }
+    }
+}
+
+// Both gradients in one pass over x and dy.  Each thread owns the same columns
+// in every row that its block takes, so the column sums stay in its registers
+// until the block's last row and leave as one row of partial sums.
+template <int EB, int NT, int UPT, int R, bool RAGGED>
+__global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
+    constexpr int E = Vec<EB>::E, W = NT / 64;
+    __shared__ float lds[2][W * 2 * R];
+    const float inv = 1.0f / (float)a.cols;
+    Place at[UPT];
+    float w[UPT][E], dw[UPT][E], db[UPT][E];
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
+        ld_params<E>(a.weight, a.pb, at[u].at, a.cols, 1.0f, w[u]);
+#pragma unroll
+        for (int j = 0; j < E; ++j) dw[u][j] = db[u][j] = 0.0f;
+    }
+    int buf = 0;
+    for (size_t r0 = (size_t)blockIdx.x * R; r0 < a.rows; r0 += (size_t)gridDim.x * R, buf ^= 1) {
+        u32x4 rx[R][UPT], rg[R][UPT];
+        float mean[R], rstd[R], s[2 * R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const size_t r = r0 + k < a.rows ? r0 + k : a.rows - 1;
+            const char* x = static_cast<const char*>(a.x) + r * a.xstride * EB;
+            const char* dy = static_cast<const char*>(a.dy) + r * a.dystride * EB;
+            mean[k] = ld_uniform(a.mean + r);
+            rstd[k] = ld_uniform(a.rstd + r);
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                const unsigned off = offset_here(at[u].at * EB);
+                rx[k][u] = ld_unit<EB, true>(x + off);
+                rg[k][u] = ld_unit<EB, true>(dy + off);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                // (a row past the last: none of its elements counts)
+                const int skip = r0 + k < a.rows ? at[u].skip : E;
+                if (skip) {
+                    rx[k][u] = drop_first<EB, RAGGED>(rx[k][u], skip);
+                    rg[k][u] = drop_first<EB, RAGGED>(rg[k][u], skip);
+                }
+                float v[E], g[E];
+                Vec<EB>::unpack(rx[k][u], v);
+                Vec<EB>::unpack(rg[k][u], g);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float xh = (v[j] - mean[k]) * rstd[k];
+                    const float gw = g[j] * w[u][j];    // 0 where dropped
+                    s1 += gw;
+                    s2 = __builtin_fmaf(gw, xh, s2);
+                    dw[u][j] = __builtin_fmaf(g[j], xh, dw[u][j]);
+                    db[u][j] += g[j];
+                }
+            }
+            s[2 * k] = s1;
+            s[2 * k + 1] = s2;
+#pragma unroll
+            for (int u = 0; u < UPT; ++u)
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    settle(dw[u][j]);
+                    settle(db[u][j]);
+                }
+            __builtin_amdgcn_sched_barrier(0);   // one row's temporaries at a time
+        }
+        block_sums<W, 2 * R>(s, lds[buf]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k >= a.rows) break;
+            const float c1 = s[2 * k] * inv, c2 = s[2 * k + 1] * inv;
+            char* dx = static_cast<char*>(a.dx) + (r0 + k) * a.cols * EB;
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                float v[E], g[E];
+                refresh(rx[k][u]);
+                refresh(rg[k][u]);
+                Vec<EB>::unpack(rx[k][u], v);
+                Vec<EB>::unpack(rg[k][u], g);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float xh = (v[j] - mean[k]) * rstd[k];
+                    v[j] = rstd[k] * __builtin_fmaf(-xh, c2, __builtin_fmaf(g[j], w[u][j], -c1));
+                }
+                st_place<EB, RAGGED, true>(dx, at[u], Vec<EB>::pack(v));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if (!a.dweight && !a.dbias) return;
+    float* out = a.part + (size_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+    for (int u = 0; u < UPT; ++u)
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if (RAGGED ? j >= at[u].skip : at[u].skip == 0) {
+                const size_t c = at[u].at + j;
+                if (gridDim.x > 1) {
+                    out[c] = dw[u][j];
+                    out[a.cols + c] = db[u][j];
+                } else {   // no other part: these are the sums
+                    if (a.dweight) st_param(a.dweight, a.pb, c, dw[u][j]);
+                    if (a.dbias) st_param(a.dbias, a.pb, c, db[u][j]);
+                }
+            }
+}
+
 // Rows of any width: one block per row, three walks over it (the second and
 // third find it in the cache).
 template <int EB>
@@ -143,24 +344,26 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_cols(const NormGradArgs a
         }
 }
 
-// The last step: the partial rows of one column added in a fixed order.
-__global__ __launch_bounds__(kNormThreads) void k_norm_fold(const NormGradArgs a, size_t parts) {
-    __shared__ float lds[kNormWaves][64];
+// The last step: the partial rows of a column added in a fixed order, 64
+// columns a block with its wavefronts side by side down the parts.
+constexpr int kFoldThreads = 1024, kFoldWaves = kFoldThreads / 64;
+__global__ __launch_bounds__(kFoldThreads) void k_norm_fold(const NormGradArgs a, size_t parts) {
+    __shared__ float lds[kFoldWaves][64];
     const unsigned lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const size_t c = (size_t)blockIdx.x * 64 + lane;   // of 2 * cols
     float s = 0.0f;
-    if (c < 2 * a.cols)
-        for (size_t p = wave; p < parts; p += kNormWaves) s += a.part[p * 2 * a.cols + c];
+    if (c < 2 * a.cols) {
+        const float* p = a.part + c;
+#pragma unroll 8
+        for (size_t k = wave; k < parts; k += kFoldWaves) s += p[k * 2 * a.cols];
+    }
     lds[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || c >= 2 * a.cols) return;
 #pragma unroll
-    for (int w = 1; w < kNormWaves; ++w) s += lds[w][lane];
+    for (int w = 1; w < kFoldWaves; ++w) s += lds[w][lane];
     void* out = c < a.cols ? a.dweight : a.dbias;
-    const size_t i = c < a.cols ? c : c - a.cols;
-    if (!out) return;
-    if (a.pb == 4) Vec<4>::st1(static_cast<char*>(out) + i * 4, s);
-    else Vec<2>::st1(static_cast<char*>(out) + i * 2, s);
+    if (out) st_param(out, a.pb, c < a.cols ? c : c - a.cols, s);
 }
 
 }  // namespace
@@ -171,45 +374,109 @@ static unsigned row_blocks(size_t rows) {
     return (unsigned)(rows < kMost ? rows : kMost);
 }
 
+// The shape of a row kernel: threads, units per thread and rows at a time;
+// threads 0: rows too wide for registers, or narrower than a unit, are the wide
+// kernels'.
+struct RowShape {
+    int threads, upt, r;
+};
+static RowShape row_shape(size_t cols, int eb) {
+    if (cols < 16u / eb) return {0, 0, 0};   // no 16 bytes in a row
+    const size_t units = (cols * eb + 15) / 16;
+    if (units <= 64) return {64, 1, 4};
+    if (units <= 256) return {256, 1, 4};
+    if (units <= 512) return {512, 1, 4};
+    if (units <= 1024) return {1024, 1, 4};
+    if (units <= 2048) return {1024, 2, 2};
+    if (units <= 4096 && eb == 4) return {1024, 4, 1};
+    return {0, 0, 0};
+}
+
+// Blocks of the backward row kernel: enough wavefronts for every compute unit
+// (16 each), but at least kRowsPerPart rows for each row of partial sums that a
+// block leaves.
+constexpr size_t kRowsPerPart = 16;
+static size_t grad_blocks(size_t rows, RowShape sh) {
+    if (rows <= kRowsPerPart) return rows ? 1 : 0;
+    const size_t most = 4096 / (sh.threads / 64), want = (rows + kRowsPerPart - 1) / kRowsPerPart;
+    return want < most ? want : most;
+}
+
 size_t norm_grad_parts(size_t rows, size_t cols, int eb) {
-    (void)cols;
-    (void)eb;
+    const RowShape sh = row_shape(cols, eb);
+    if (sh.threads) return grad_blocks(rows, sh);
     const size_t p = (rows + kColRows - 1) / kColRows;
     return p < kColParts ? p : kColParts;
 }
 
+#define ROWS_BY_SHAPE(EB, RAGGED, CALL)                                       \
+    switch (sh.threads * 8 + sh.upt) {                                        \
+        case 64 * 8 + 1: CALL(EB, 64, 1, 4, RAGGED); break;                   \
+        case 256 * 8 + 1: CALL(EB, 256, 1, 4, RAGGED); break;                 \
+        case 512 * 8 + 1: CALL(EB, 512, 1, 4, RAGGED); break;                 \
+        case 1024 * 8 + 1: CALL(EB, 1024, 1, 4, RAGGED); break;               \
+        case 1024 * 8 + 2: CALL(EB, 1024, 2, 2, RAGGED); break;               \
+        default: if constexpr (EB == 4) CALL(EB, 1024, 4, 1, RAGGED); break;  \
+    }
+// RAGGED: the row's end lies inside a unit (the other form spends no
+// registers on that)
+#define ROWS_BY_TYPE(CALL)                                      \
+    if (a.cols % (16 / a.eb) == 0) {                            \
+        if (a.eb == 2) { ROWS_BY_SHAPE(2, false, CALL) } else { ROWS_BY_SHAPE(4, false, CALL) } \
+    } else {                                                    \
+        if (a.eb == 2) { ROWS_BY_SHAPE(2, true, CALL) } else { ROWS_BY_SHAPE(4, true, CALL) } \
+    }
+
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
+    const RowShape sh = row_shape(a.cols, a.eb);
+    if (sh.threads == 0) {
+        const dim3 grid(row_blocks(a.rows)), block(kNormThreads);
+        if (a.eb == 2) hipLaunchKernelGGL(k_norm_wide<2>, grid, block, 0, s, a);
+        else hipLaunchKernelGGL(k_norm_wide<4>, grid, block, 0, s, a);
+        return hipGetLastError();
+    }
+    const dim3 grid(row_blocks((a.rows + sh.r - 1) / sh.r)), block(sh.threads);
+#define CALL(EB, NT, UPT, R, RAGGED) \
+    hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, R, RAGGED>), grid, block, 0, s, a)
+    ROWS_BY_TYPE(CALL)
+#undef CALL
+    return hipGetLastError();
+}
+
+static hipError_t launch_grad_wide(const NormGradArgs& a, size_t parts, hipStream_t s) {
     const dim3 grid(row_blocks(a.rows)), block(kNormThreads);
-    if (a.eb == 2) hipLaunchKernelGGL(k_norm_wide<2>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_norm_wide<4>, grid, block, 0, s, a);
+    if (a.eb == 2) hipLaunchKernelGGL(k_norm_grad_wide<2>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(k_norm_grad_wide<4>, grid, block, 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!a.dweight && !a.dbias)) return e;
+    const size_t per = (size_t)kNormThreads * (16 / a.eb);
+    const size_t rows_per = (a.rows + parts - 1) / parts;
+    const dim3 g2((unsigned)((a.cols + per - 1) / per), (unsigned)parts);
+    if (a.eb == 2) hipLaunchKernelGGL(k_norm_cols<2>, g2, block, 0, s, a, rows_per);
+    else hipLaunchKernelGGL(k_norm_cols<4>, g2, block, 0, s, a, rows_per);
     return hipGetLastError();
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
     const size_t parts = norm_grad_parts(a.rows, a.cols, a.eb);
-    if (a.rows > 0) {
-        const dim3 grid(row_blocks(a.rows)), block(kNormThreads);
-        if (a.eb == 2) hipLaunchKernelGGL(k_norm_grad_wide<2>, grid, block, 0, s, a);
-        else hipLaunchKernelGGL(k_norm_grad_wide<4>, grid, block, 0, s, a);
-        hipError_t e = hipGetLastError();
+    const RowShape sh = row_shape(a.cols, a.eb);
+    if (a.rows > 0 && sh.threads) {
+        const dim3 grid((unsigned)parts), block(sh.threads);
+#define CALL(EB, NT, UPT, R, RAGGED) \
+    hipLaunchKernelGGL((k_norm_grad_rows<EB, NT, UPT, R, RAGGED>), grid, block, 0, s, a)
+        ROWS_BY_TYPE(CALL)
+#undef CALL
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || parts == 1) return e;
+    } else if (a.rows > 0) {
+        const hipError_t e = launch_grad_wide(a, parts, s);
         if (e != hipSuccess) return e;
-        if (a.dweight || a.dbias) {
-            const size_t per = (size_t)kNormThreads * (16 / a.eb);
-            const size_t rows_per = (a.rows + parts - 1) / parts;
-            const dim3 g2((unsigned)((a.cols + per - 1) / per), (unsigned)parts);
-            if (a.eb == 2) hipLaunchKernelGGL(k_norm_cols<2>, g2, block, 0, s, a, rows_per);
-            else hipLaunchKernelGGL(k_norm_cols<4>, g2, block, 0, s, a, rows_per);
-            e = hipGetLastError();
-            if (e != hipSuccess) return e;
-        }
     }
-    if (a.dweight || a.dbias) {
-        hipLaunchKernelGGL(k_norm_fold, dim3((unsigned)((2 * a.cols + 63) / 64)),
-                           dim3(kNormThreads), 0, s, a, parts);
-        return hipGetLastError();
-    }
-    return hipSuccess;
+    if (!a.dweight && !a.dbias) return hipSuccess;
+    hipLaunchKernelGGL(k_norm_fold, dim3((unsigned)((2 * a.cols + 63) / 64)), dim3(kFoldThreads), 0,
+                       s, a, parts);
+    return hipGetLastError();
 }
 
 }  // namespace arlib

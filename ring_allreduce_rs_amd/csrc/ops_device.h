@@ -118,6 +118,58 @@ __device__ __forceinline__ void st_unit_of(char* row, size_t i, size_t n, u32x4 
     }
 }
 
+// A byte offset that the compiler takes as new here: added to a uniform
+// pointer it stays the 32-bit offset of the load or store, where a 64-bit sum
+// kept across a loop would take two registers for each access.
+__device__ __forceinline__ unsigned offset_here(unsigned v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Where a thread's unit lies in a row of n >= E elements when the unit at
+// element i is its share: a share that runs past the end moves back to the
+// row's last E elements, and its first `skip` ones are another thread's.  The
+// load is then the same for every thread, without a branch; the last unit's
+// owner alone drops what is not its own.
+struct Place {
+    unsigned at;   // first element of the 16 bytes
+    int skip;      // elements that are not this thread's (E: none is)
+};
+template <int E>
+__device__ __forceinline__ Place place_unit(unsigned i, unsigned n) {
+    Place p;
+    p.at = i + E <= n ? i : n - E;
+    p.skip = (int)(i - p.at < (unsigned)E ? i - p.at : (unsigned)E);
+    return p;
+}
+// u with its first `skip` > 0 elements 0.  Where rows end at a unit's end
+// (RAGGED false), skip is all of them or none.
+template <int EB, bool RAGGED>
+__device__ __forceinline__ u32x4 drop_first(u32x4 u, int skip) {
+    if constexpr (!RAGGED) return u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (EB == 4) u[i] = i < skip ? 0u : u[i];
+        else u[i] = 2 * i + 1 < skip ? 0u : 2 * i < skip ? u[i] & 0xffff0000u : u[i];
+    }
+    return u;
+}
+// Stores this thread's elements of u to the row.
+template <int EB, bool RAGGED, bool NT = false>
+__device__ __forceinline__ void st_place(char* row, Place p, u32x4 u) {
+    if (p.skip == 0) {
+        st_unit<EB, NT>(row + offset_here(p.at * EB), u);
+    } else if (RAGGED) {
+#pragma unroll
+        for (int j = 1; j < Vec<EB>::E; ++j)
+            if (j >= p.skip) {
+                char* q = row + offset_here((p.at + j) * EB);
+                if constexpr (EB == 4) st_elem<4>(q, u[j]);
+                else st_elem<2>(q, (j & 1) ? u[j / 2] >> 16 : u[j / 2] & 0xffffu);
+            }
+    }
+}
+
 // E parameters (weight, bias) at column i of n, `pb` bytes each; past the end
 // and for a NULL array they are `none`.
 template <int E>
@@ -153,18 +205,58 @@ __device__ __forceinline__ void ld_params(const void* base, int pb, size_t i, si
     }
 }
 
-// Sum over the 64 lanes, on every lane.  A butterfly: every lane adds the same
-// pairs, so the lanes agree to the last bit.
+// Ends the reuse of values computed from u: what is needed of them later is
+// computed again from the 16 bytes, where the compiler would hold 4 times as
+// many registers across a barrier.
+__device__ __forceinline__ void refresh(u32x4& u) { asm volatile("" : "+v"(u)); }
+
+// Has v computed by here (an accumulator's update would else be put off, and
+// its operands kept, past a barrier).
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
+
+// A value at a uniform address that no store of this kernel changes.
+__device__ __forceinline__ float ld_uniform(const float* p) {
+    typedef const float __attribute__((address_space(4))) * constant_t;
+    return *(constant_t)(uintptr_t)p;
+}
+
+// Sum and maximum over the 64 lanes, the same on every lane.  Lanes are joined
+// with DPP moves (inside rows of 16, then across them towards lane 63), which
+// cost one instruction a step where a shuffle goes through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v) {
+    return as_f32((uint32_t)__builtin_amdgcn_update_dpp((int)as_u32(old), (int)as_u32(v), CTRL, ROWS,
+                                                        0xf, false));
+}
+constexpr int kDppSwap1 = 0xb1;         // quad_perm [1, 0, 3, 2]
+constexpr int kDppSwap2 = 0x4e;         // quad_perm [2, 3, 0, 1]
+constexpr int kDppHalfMirror = 0x141;   // lane i of 8 from lane 7 - i
+constexpr int kDppMirror = 0x140;       // lane i of 16 from lane 15 - i
+constexpr int kDppLast15 = 0x142;       // lane 15 of the row before
+constexpr int kDppLast31 = 0x143;       // lane 31
+
+__device__ __forceinline__ float lane63(float v) {
+    return as_f32((uint32_t)__builtin_amdgcn_readlane((int)as_u32(v), 63));
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+    v += dpp<kDppSwap1, 0xf>(0.0f, v);
+    v += dpp<kDppSwap2, 0xf>(0.0f, v);
+    v += dpp<kDppHalfMirror, 0xf>(0.0f, v);
+    v += dpp<kDppMirror, 0xf>(0.0f, v);
+    v += dpp<kDppLast15, 0xa>(0.0f, v);   // rows 1 and 3
+    v += dpp<kDppLast31, 0xc>(0.0f, v);   // rows 2 and 3
+    return lane63(v);
 }
 
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
+    v = fmaxf(v, dpp<kDppSwap1, 0xf>(v, v));
+    v = fmaxf(v, dpp<kDppSwap2, 0xf>(v, v));
+    v = fmaxf(v, dpp<kDppHalfMirror, 0xf>(v, v));
+    v = fmaxf(v, dpp<kDppMirror, 0xf>(v, v));
+    v = fmaxf(v, dpp<kDppLast15, 0xa>(v, v));
+    v = fmaxf(v, dpp<kDppLast31, 0xc>(v, v));
+    return lane63(v);
 }
 
 // Sum over a block of W wavefronts, on every thread.  `lds` holds W floats and
@@ -179,6 +271,34 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
 #pragma unroll
     for (int w = 1; w < W; ++w) t += lds[w];
     return t;
+}
+
+// V sums over a block of W wavefronts at once (V a power of two), on every
+// thread.  `lds` holds W * V floats; the barrier inside is the only one, so a
+// caller that comes back before another barrier takes another buffer.
+template <int W, int V>
+__device__ __forceinline__ void block_sums(float (&v)[V], float* lds) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = wave_sum(v[i]);
+    if constexpr (W > 1) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        float mine = v[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) mine = lane == i ? v[i] : mine;
+        if (lane < V) lds[wave * V + lane] = mine;
+        __syncthreads();
+        // lane l takes sum l % V of every (64 / V)th wavefront
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; w += 64 / V)
+            if (w + lane / V < W) t += lds[w * V + lane];
+#pragma unroll
+        for (int d = V; d < 64; d <<= 1)
+            if (d / V < W) t += __shfl_xor(t, d, 64);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = as_f32((uint32_t)__builtin_amdgcn_readlane((int)as_u32(t), i));
+    }
 }
 
 }  // namespace arlib
