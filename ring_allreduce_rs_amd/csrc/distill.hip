@@ -277,6 +277,138 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
     }
 }
 
+// Loss and gradient of rows that a block holds in registers: UPT units a
+// thread.  A block takes row after row, and while it turns one row's units into
+// gradients it loads the next row's into the registers that become free, so
+// that loads, exponentials and stores of one compute unit overlap although a
+// row may fill most of its registers.  Thread j keeps teacher entries j,
+// j + NT, ... (one, unless the block is small).
+//
+// Sums are joined over the wavefronts at barrier A; barrier B comes between the
+// row's stores and those of the kept entries, which write their places again
+// with q - p.
+struct RowSums {
+    float m[16], s[16], tm[16], ts[16], loss[16];
+};
+// A wavefront's maximum and sum over its lanes'.
+__device__ __forceinline__ Soft wave_soft(Soft v, float c) {
+    const float m = wave_max(v.m);
+    return {m, wave_sum(v.s * exp2_fast((soft_from(v.m) - soft_base(m)) * c))};
+}
+
+template <int EB, int IB, int UPT>
+__global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
+    constexpr int E = Vec<EB>::E;
+    constexpr uint32_t kNinf = EB == 2 ? 0xff80ff80u : 0xff800000u;
+    __shared__ RowSums red;
+    __shared__ int at[kMaxTop];
+    __shared__ float tz[kMaxTop];
+    const int nt = blockDim.x, waves = nt >> 6, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int top = (int)a.top;
+    const float c = kLog2e / a.temperature;
+    u32x4 raw[UPT];
+    // (worked out where it is used: kept, the masks of all units would take
+    // more scalar registers than there are)
+    const auto place = [&](int u) {
+        return place_unit<E>((u * nt + offset_here(threadIdx.x)) * E, (unsigned)a.vocab);
+    };
+    size_t r = blockIdx.x;
+    {
+        const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) raw[u] = ld_unit<EB, true>(z + place(u).at * EB);
+    }
+    for (; r < a.rows; r += gridDim.x) {
+        const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
+        const char* t = static_cast<const char*>(a.teacher) + r * a.top * EB;
+        // the teacher's entries, and this thread's share of both sums
+        Soft ts = soft_zero();
+        for (int j = threadIdx.x; j < top; j += nt) {
+            const int v = place_of<IB>(a.indices, r * a.top + j, a.vocab);
+            const float x = v >= 0 ? Vec<EB>::ld1(t + (size_t)j * EB) : -INFINITY;
+            at[j] = v;
+            tz[j] = x;
+            const float one[1] = {x};
+            soft_add<1>(ts, one, c);
+        }
+        Soft zs = soft_zero();
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) {
+            const int skip = place(u).skip;
+            if (skip) raw[u] = fill_first<EB>(raw[u], skip, kNinf);
+            float v[E];
+            Vec<EB>::unpack(raw[u], v);
+            soft_add<E>(zs, v, c);
+        }
+        zs = wave_soft(zs, c);
+        ts = wave_soft(ts, c);
+        if (lane == 0) {
+            red.m[wave] = zs.m;
+            red.s[wave] = zs.s;
+            red.tm[wave] = ts.m;
+            red.ts[wave] = ts.s;
+        }
+        __syncthreads();   // A
+        const bool has = lane < waves;
+        zs = wave_soft(Soft{has ? red.m[lane & 15] : -INFINITY, has ? red.s[lane & 15] : 0.0f}, c);
+        ts = wave_soft(Soft{has ? red.tm[lane & 15] : -INFINITY, has ? red.ts[lane & 15] : 0.0f}, c);
+        const bool some = !(ts.s == 0.0f);
+        const float lse = soft_lse(zs, a.temperature), scale = a.dloss[r] * a.temperature;
+        const float tbase = soft_base(ts.m), tinv = 1.0f / ts.s, logs = logf(ts.s);
+        const float base = soft_base(zs.m), gain = 1.0f / zs.s * scale;
+        float loss = 0.0f;
+        if (some)
+            for (int j = threadIdx.x; j < top; j += nt) {
+                const float p = exp2_fast((tz[j] - tbase) * c) * tinv;
+                if (at[j] < 0 || p == 0.0f) continue;
+                const float logp = (tz[j] - tbase) / a.temperature - logs;
+                const float logq = Vec<EB>::ld1(z + (size_t)at[j] * EB) / a.temperature - lse;
+                loss = __builtin_fmaf(p, logp - logq, loss);
+            }
+        loss = wave_sum(loss);
+        if (lane == 0) red.loss[wave] = loss;
+
+        // the row's gradient; the next row's units take the registers
+        const bool more = r + gridDim.x < a.rows;
+        const char* zn = z + (size_t)gridDim.x * a.lstride * EB;
+        char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) {
+            float v[E];
+            refresh(raw[u]);
+            Vec<EB>::unpack(raw[u], v);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = some ? exp2_fast((v[j] - base) * c) * gain : 0.0f;
+            const Place pl = place(u);
+            st_place<EB, true, true>(dz, pl, Vec<EB>::pack(v));
+            if (more) raw[u] = ld_unit<EB, true>(zn + pl.at * EB);
+        }
+        __syncthreads();   // B
+        if (some)
+            for (int j = threadIdx.x; j < top; j += nt) {
+                if (at[j] < 0) continue;
+                float p = 0.0f;
+                bool first = true;
+                for (int k = 0; k < top; ++k)
+                    if (at[k] == at[j]) {
+                        first &= k >= j;
+                        p += exp2_fast((tz[k] - tbase) * c) * tinv;
+                    }
+                if (first) {
+                    const float q = exp2_fast((Vec<EB>::ld1(z + (size_t)at[j] * EB) - base) * c) /
+                                    zs.s;
+                    Vec<EB>::st1(dz + (size_t)at[j] * EB, (q - p) * scale);
+                }
+            }
+        if (threadIdx.x == 0) {
+            float sum = 0.0f;
+            for (int w = 0; w < waves; ++w) sum += red.loss[w];
+            a.loss[r] = some ? sum * (a.temperature * a.temperature) : 0.0f;
+        }
+        __syncthreads();   // at, tz and red are free
+    }
+}
+
 // The split of a row into chunks: kChunkBytes, more blocks for few rows.
 struct Split {
     size_t parts, chunk;
@@ -289,6 +421,26 @@ Split split_of(size_t rows, size_t vocab, int eb) {
     size_t chunk = (vocab + parts - 1) / parts;
     chunk = (chunk + e - 1) / e * e;
     return {(vocab + chunk - 1) / chunk, chunk};
+}
+
+// The register form of a step: units per thread and threads; upt 0: the row
+// does not fit (or is shorter than a unit), the two-pass form takes it.  Fewer
+// units a thread give a row more threads, which pays while the rows are too few
+// to fill the card's compute units.
+constexpr int kCUs = 256;
+struct RowFit {
+    int upt, threads;
+};
+RowFit row_fit(size_t rows, size_t vocab, int eb) {
+    const size_t e = 16 / eb, units = (vocab + e - 1) / e;
+    if (vocab < e) return {0, 0};
+    for (int upt = 16; upt >= 4; upt /= 2) {
+        const size_t nt = (((units + upt - 1) / upt) + 63) / 64 * 64;
+        if (nt > 1024) break;
+        if (upt == 4 || rows * nt >= (size_t)kCUs * 1024) return {upt, (int)nt};
+        if ((((units + upt / 2 - 1) / (upt / 2)) + 63) / 64 * 64 > 1024) return {upt, (int)nt};
+    }
+    return {0, 0};
 }
 
 unsigned grid_of(size_t tasks) {
@@ -314,8 +466,7 @@ hipError_t launch_part(const DistillArgs& a, Split sp, hipStream_t s) {
 }  // namespace
 
 size_t distill_work_floats(size_t rows, size_t vocab, int eb, bool step) {
-    (void)step;
-    if (rows == 0) return 0;
+    if (rows == 0 || (step && row_fit(rows, vocab, eb).upt)) return 0;
     return 2 * rows * split_of(rows, vocab, eb).parts;
 }
 
@@ -345,6 +496,19 @@ hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s) {
 
 hipError_t launch_distill_step(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
+    const RowFit fit = row_fit(a.rows, a.vocab, a.eb);
+    if (fit.upt) {
+        // as many blocks as run at once: 16 wavefronts a compute unit
+        const size_t most = (size_t)kCUs * 1024 / fit.threads;
+        const dim3 grid((unsigned)(a.rows < most ? a.rows : most)), block(fit.threads);
+#define CALL(EB, IB)                                                                             \
+    if (fit.upt == 4) hipLaunchKernelGGL((k_distill_rows<EB, IB, 4>), grid, block, 0, s, a);     \
+    else if (fit.upt == 8) hipLaunchKernelGGL((k_distill_rows<EB, IB, 8>), grid, block, 0, s, a); \
+    else hipLaunchKernelGGL((k_distill_rows<EB, IB, 16>), grid, block, 0, s, a)
+        DISTILL_BY_TYPE(CALL);
+#undef CALL
+        return hipGetLastError();
+    }
     const Split sp = split_of(a.rows, a.vocab, a.eb);
     const hipError_t e = launch_part(a, sp, s);
     if (e != hipSuccess) return e;

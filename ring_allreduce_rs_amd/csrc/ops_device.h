@@ -154,6 +154,19 @@ __device__ __forceinline__ u32x4 drop_first(u32x4 u, int skip) {
     }
     return u;
 }
+// u with its first `skip` elements replaced by those of the word `fill`
+template <int EB>
+__device__ __forceinline__ u32x4 fill_first(u32x4 u, int skip, uint32_t fill) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (EB == 4) u[i] = i < skip ? fill : u[i];
+        else
+            u[i] = 2 * i + 1 < skip ? fill
+                   : 2 * i < skip   ? (u[i] & 0xffff0000u) | (fill & 0xffffu)
+                                    : u[i];
+    }
+    return u;
+}
 // Stores this thread's elements of u to the row.
 template <int EB, bool RAGGED, bool NT = false>
 __device__ __forceinline__ void st_place(char* row, Place p, u32x4 u) {
