@@ -281,12 +281,14 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
 // thread.  A block takes row after row, and while it turns one row's units into
 // gradients it loads the next row's into the registers that become free, so
 // that loads, exponentials and stores of one compute unit overlap although a
-// row may fill most of its registers.  Thread j keeps teacher entries j,
-// j + NT, ... (one, unless the block is small).
+// row may fill most of its registers.
 //
-// Sums are joined over the wavefronts at barrier A; barrier B comes between the
-// row's stores and those of the kept entries, which write their places again
-// with q - p.
+// Thread j keeps teacher entry j of the row (and, in blocks of fewer threads
+// than entries, walks the others); the next row's entries are loaded among its
+// units.  There is one barrier a row: before it every wavefront leaves its sums
+// of this row, after it the entries' places of the row before are written again
+// with q - p (its plain gradients were all stored before the barrier) and its
+// loss is added up.  What one row leaves in LDS the next but one replaces.
 struct RowSums {
     float m[16], s[16], tm[16], ts[16], loss[16];
 };
@@ -295,16 +297,42 @@ __device__ __forceinline__ Soft wave_soft(Soft v, float c) {
     const float m = wave_max(v.m);
     return {m, wave_sum(v.s * exp2_fast((soft_from(v.m) - soft_base(m)) * c))};
 }
+// G units added to a thread's share.  Values are taken from the maximum before
+// they are scaled: scaled first (one fma less), a row of the type's lowest
+// value would overflow.
+template <int EB, int G>
+__device__ __forceinline__ void soft_units(Soft& a, const u32x4* u, float c) {
+    constexpr int E = Vec<EB>::E;
+    float m = a.m;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float v[E];
+        Vec<EB>::unpack(u[g], v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) m = fmaxf(m, v[j]);
+    }
+    const float base = soft_base(m);
+    float s = a.s * exp2_fast((soft_from(a.m) - base) * c);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float v[E];
+        Vec<EB>::unpack(u[g], v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) s += exp2_fast((v[j] - base) * c);
+    }
+    a.m = m;
+    a.s = s;
+}
 
 template <int EB, int IB, int UPT>
 __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     constexpr int E = Vec<EB>::E;
     constexpr uint32_t kNinf = EB == 2 ? 0xff80ff80u : 0xff800000u;
-    __shared__ RowSums red;
-    __shared__ int at[kMaxTop];
-    __shared__ float tz[kMaxTop];
+    __shared__ RowSums red[2];
+    __shared__ int at[2][kMaxTop];
+    __shared__ float tz[2][kMaxTop];
     const int nt = blockDim.x, waves = nt >> 6, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int top = (int)a.top;
+    const int top = (int)a.top, tid = threadIdx.x;
     const float c = kLog2e / a.temperature;
     u32x4 raw[UPT];
     // (worked out where it is used: kept, the masks of all units would take
@@ -312,101 +340,176 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     const auto place = [&](int u) {
         return place_unit<E>((u * nt + offset_here(threadIdx.x)) * E, (unsigned)a.vocab);
     };
+    const auto logit = [&](size_t r, int v) {
+        return Vec<EB>::ld1(static_cast<const char*>(a.logits) + (r * a.lstride + v) * EB);
+    };
+    const auto entry = [&](size_t r, int j, float* x) {
+        const int v = place_of<IB>(a.indices, r * a.top + j, a.vocab);
+        *x = Vec<EB>::ld1(static_cast<const char*>(a.teacher) + (r * a.top + j) * EB);
+        return v;
+    };
+
     size_t r = blockIdx.x;
+    int my_at = -1;                 // this thread's entry of the row
+    float my_t = -INFINITY, my_z = 0.0f;
+    if (tid < top) {
+        my_at = entry(r, tid, &my_t);
+        if (my_at >= 0) my_z = logit(r, my_at);
+    }
     {
         const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
 #pragma unroll
         for (int u = 0; u < UPT; ++u) raw[u] = ld_unit<EB, true>(z + place(u).at * EB);
     }
-    for (; r < a.rows; r += gridDim.x) {
-        const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
-        const char* t = static_cast<const char*>(a.teacher) + r * a.top * EB;
-        // the teacher's entries, and this thread's share of both sums
-        Soft ts = soft_zero();
-        for (int j = threadIdx.x; j < top; j += nt) {
-            const int v = place_of<IB>(a.indices, r * a.top + j, a.vocab);
-            const float x = v >= 0 ? Vec<EB>::ld1(t + (size_t)j * EB) : -INFINITY;
-            at[j] = v;
-            tz[j] = x;
-            const float one[1] = {x};
-            soft_add<1>(ts, one, c);
+    const auto stage = [&](size_t row, int b) {
+        if (tid < top) {
+            my_t = my_at >= 0 ? my_t : -INFINITY;
+            at[b][tid] = my_at;
+            tz[b][tid] = my_t;
         }
-        Soft zs = soft_zero();
+        for (int j = tid + nt; j < top; j += nt) {
+            float x;
+            const int v = entry(row, j, &x);
+            at[b][j] = v;
+            tz[b][j] = v >= 0 ? x : -INFINITY;
+        }
+    };
+    stage(r, 0);
+
+    // the entry of the row before that is still to be written, and its loss
+    bool owed = false;
+    char* owed_at = nullptr;
+    float owed_v = 0.0f;
+    int b = 0;
+    bool some_before = false;
+    const auto settle_row = [&](size_t row, int rb) {
+        if (owed) Vec<EB>::st1(owed_at, owed_v);
+        if (tid == 0) {
+            float sum = 0.0f;
+            for (int w = 0; w < waves; ++w) sum += red[rb].loss[w];
+            a.loss[row] = some_before ? sum * (a.temperature * a.temperature) : 0.0f;
+        }
+    };
+
+    for (; r < a.rows; r += gridDim.x, b ^= 1) {
+        // this wavefront's share of both sums
+        Soft zs = soft_zero(), ts = soft_zero();
+        constexpr int G = UPT < 4 ? UPT : 4;
 #pragma unroll
-        for (int u = 0; u < UPT; ++u) {
-            const int skip = place(u).skip;
-            if (skip) raw[u] = fill_first<EB>(raw[u], skip, kNinf);
-            float v[E];
-            Vec<EB>::unpack(raw[u], v);
-            soft_add<E>(zs, v, c);
+        for (int u = 0; u < UPT; u += G) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int skip = place(u + g).skip;
+                if (skip) raw[u + g] = fill_first<EB>(raw[u + g], skip, kNinf);
+            }
+            soft_units<EB, G>(zs, raw + u, c);
+        }
+        for (int j = tid; j < top; j += nt) {
+            const float one[1] = {tz[b][j]};
+            soft_add<1>(ts, one, c);
         }
         zs = wave_soft(zs, c);
         ts = wave_soft(ts, c);
         if (lane == 0) {
-            red.m[wave] = zs.m;
-            red.s[wave] = zs.s;
-            red.tm[wave] = ts.m;
-            red.ts[wave] = ts.s;
+            red[b].m[wave] = zs.m;
+            red[b].s[wave] = zs.s;
+            red[b].tm[wave] = ts.m;
+            red[b].ts[wave] = ts.s;
         }
-        __syncthreads();   // A
+        __syncthreads();
+        if (r >= gridDim.x) settle_row(r - gridDim.x, b ^ 1);
         const bool has = lane < waves;
-        zs = wave_soft(Soft{has ? red.m[lane & 15] : -INFINITY, has ? red.s[lane & 15] : 0.0f}, c);
-        ts = wave_soft(Soft{has ? red.tm[lane & 15] : -INFINITY, has ? red.ts[lane & 15] : 0.0f}, c);
+        const int w = lane & 15;
+        zs = wave_soft({has ? red[b].m[w] : -INFINITY, has ? red[b].s[w] : 0.0f}, c);
+        ts = wave_soft({has ? red[b].tm[w] : -INFINITY, has ? red[b].ts[w] : 0.0f}, c);
         const bool some = !(ts.s == 0.0f);
-        const float lse = soft_lse(zs, a.temperature), scale = a.dloss[r] * a.temperature;
-        const float tbase = soft_base(ts.m), tinv = 1.0f / ts.s, logs = logf(ts.s);
-        const float base = soft_base(zs.m), gain = 1.0f / zs.s * scale;
+        const float scale = a.dloss[r] * a.temperature;
+        const float base = soft_base(zs.m), lse = soft_lse(zs, a.temperature);
+        const float tbase = soft_base(ts.m), logs = logf(ts.s), tinv = 1.0f / ts.s;
+        char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;
+
+        // loss terms, and the value that an entry's place gets
+        const auto prob = [&](int j) { return exp2_fast((tz[b][j] - tbase) * c) * tinv; };
+        const auto term = [&](int j, float zj) {
+            const float p = prob(j);
+            if (at[b][j] < 0 || p == 0.0f) return 0.0f;
+            return p * ((tz[b][j] - tbase) / a.temperature - logs - (zj / a.temperature - lse));
+        };
+        const auto patch = [&](int j, float zj, float* v) {
+            const int mine = at[b][j];
+            float p = 0.0f;
+            bool first = mine >= 0;
+            for (int k = 0; k < top; ++k)
+                if (at[b][k] == mine) {
+                    first &= k >= j;
+                    p += prob(k);
+                }
+            *v = (exp2_fast((zj - base) * c) / zs.s - p) * scale;
+            return first;
+        };
         float loss = 0.0f;
-        if (some)
-            for (int j = threadIdx.x; j < top; j += nt) {
-                const float p = exp2_fast((tz[j] - tbase) * c) * tinv;
-                if (at[j] < 0 || p == 0.0f) continue;
-                const float logp = (tz[j] - tbase) / a.temperature - logs;
-                const float logq = Vec<EB>::ld1(z + (size_t)at[j] * EB) / a.temperature - lse;
-                loss = __builtin_fmaf(p, logp - logq, loss);
+        owed = false;
+        some_before = some;
+        if (some) {
+            if (tid < top) {
+                loss = term(tid, my_z);
+                owed = patch(tid, my_z, &owed_v);
+                owed_at = dz + (size_t)(my_at < 0 ? 0 : my_at) * EB;
             }
+            for (int j = tid + nt; j < top; j += nt)
+                if (at[b][j] >= 0) loss += term(j, logit(r, at[b][j]));
+        }
         loss = wave_sum(loss);
-        if (lane == 0) red.loss[wave] = loss;
+        if (lane == 0) red[b].loss[wave] = loss;
 
         // the row's gradient; the next row's units take the registers
         const bool more = r + gridDim.x < a.rows;
-        const char* zn = z + (size_t)gridDim.x * a.lstride * EB;
-        char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;
+        const size_t next = r + gridDim.x;
+        const char* zn = static_cast<const char*>(a.logits) + next * a.lstride * EB;
+        if (more && tid < top) my_at = entry(next, tid, &my_t);
+        const float gain = scale / zs.s, bias = log2f(fabsf(gain));
+        const uint32_t sign = as_u32(scale) & 0x80000000u, sign2 = sign | (sign >> 16);
 #pragma unroll
         for (int u = 0; u < UPT; ++u) {
-            float v[E];
+            u32x4 out = {0u, 0u, 0u, 0u};
             refresh(raw[u]);
-            Vec<EB>::unpack(raw[u], v);
+            if (some) {
+                float v[E];
+                Vec<EB>::unpack(raw[u], v);
+                if constexpr (EB == 2) {
+                    // |gain| goes into the exponent, where fp32 still holds
+                    // 2^-18 of a value: bf16 rounds at 2^-8
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = some ? exp2_fast((v[j] - base) * c) * gain : 0.0f;
-            const Place pl = place(u);
-            st_place<EB, true, true>(dz, pl, Vec<EB>::pack(v));
-            if (more) raw[u] = ld_unit<EB, true>(zn + pl.at * EB);
-        }
-        __syncthreads();   // B
-        if (some)
-            for (int j = threadIdx.x; j < top; j += nt) {
-                if (at[j] < 0) continue;
-                float p = 0.0f;
-                bool first = true;
-                for (int k = 0; k < top; ++k)
-                    if (at[k] == at[j]) {
-                        first &= k >= j;
-                        p += exp2_fast((tz[k] - tbase) * c) * tinv;
-                    }
-                if (first) {
-                    const float q = exp2_fast((Vec<EB>::ld1(z + (size_t)at[j] * EB) - base) * c) /
-                                    zs.s;
-                    Vec<EB>::st1(dz + (size_t)at[j] * EB, (q - p) * scale);
+                    for (int j = 0; j < E; ++j)
+                        v[j] = exp2_fast(__builtin_fmaf(v[j] - base, c, bias));
+                    out = Vec<EB>::pack(v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) out[i] ^= sign2;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        v[j] = exp2_fast((v[j] - base) * c) * gain;
+                    out = Vec<EB>::pack(v);
                 }
             }
-        if (threadIdx.x == 0) {
-            float sum = 0.0f;
-            for (int w = 0; w < waves; ++w) sum += red.loss[w];
-            a.loss[r] = some ? sum * (a.temperature * a.temperature) : 0.0f;
+            const Place pl = place(u);
+            st_place<EB, true, true>(dz, pl, out);
+            if (more) raw[u] = ld_unit<EB, true>(zn + pl.at * EB);
+            if (u == UPT / 2 && more && tid < top && my_at >= 0) my_z = logit(next, my_at);
         }
-        __syncthreads();   // at, tz and red are free
+        if (more) stage(next, b ^ 1);
+        if (top > nt) {   // the entries beyond this thread's first
+            __syncthreads();
+            for (int j = tid + nt; some && j < top; j += nt)
+                if (at[b][j] >= 0) {
+                    float v;
+                    if (patch(j, logit(r, at[b][j]), &v))
+                        Vec<EB>::st1(dz + (size_t)at[b][j] * EB, v);
+                }
+        }
     }
+    __syncthreads();
+    if (r >= gridDim.x) settle_row(r - gridDim.x, b ^ 1);
 }
 
 // The split of a row into chunks: kChunkBytes, more blocks for few rows.
