@@ -485,8 +485,8 @@ ar_status ar_layer_norm_backward_workspace(size_t rows, size_t cols, ar_dtype dt
  *   rows[j]     = x[slot[j] / topk] for j < offsets[experts], zeros beyond
  * dest and slot: int32, tokens * topk; offsets: int32, experts + 1; rows:
  * tokens * topk rows of `hidden` elements.  Limits (AR_ERR_UNSUPPORTED):
- * experts <= AR_MAX_EXPERTS, tokens * topk <= 2^31 - 1.  topk, experts and
- * hidden > 0.  With tokens == 0 only offsets (zeros) is written. */
+ * experts <= AR_MAX_EXPERTS, hidden <= 2^28, tokens * topk <= 2^31 - 1.
+ * topk, experts and hidden > 0.  With tokens == 0 only offsets (zeros) is written. */
 #define AR_MAX_EXPERTS 1024
 ar_status ar_expert_dispatch(ar_ctx* ctx, const void* x, size_t x_stride, const void* ids,
                              int index_bytes, size_t tokens, int topk, int experts, size_t hidden,

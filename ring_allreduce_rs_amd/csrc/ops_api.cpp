@@ -23,6 +23,10 @@ size_t float_bytes(int dtype) {
     return dtype == AR_BFLOAT16 ? 2 : dtype == AR_FLOAT32 ? 4 : 0;
 }
 
+// Widest row of a layer norm and of the experts (byte offsets within a row stay
+// below 2^32, and so do the column sums' threads).
+constexpr size_t kMostCols = size_t(1) << 28;
+
 // *out = a * b, false on overflow.
 bool times(size_t a, size_t b, size_t* out) { return !__builtin_mul_overflow(a, b, out); }
 
@@ -122,9 +126,6 @@ ar_status guarded(ar_ctx* ctx, F body) {
     }
 }
 
-// Widest row of a layer norm (the column sums' grid stays far below 2^32 threads).
-constexpr size_t kMostCols = size_t(1) << 28;
-
 size_t norm_workspace(size_t rows, size_t cols, size_t eb) {
     return arlib::norm_grad_parts(rows, cols, (int)eb) * 2 * cols * sizeof(float);
 }
@@ -139,6 +140,8 @@ ar_status check_route(ar_ctx* ctx, size_t tokens, int topk, int experts, size_t 
     if (hidden < 1) return fail(ctx, AR_ERR_INVALID_ARG, "hidden is 0");
     if (experts > AR_MAX_EXPERTS)
         return fail(ctx, AR_ERR_UNSUPPORTED, "experts %d above %d", experts, AR_MAX_EXPERTS);
+    if (hidden > kMostCols)
+        return fail(ctx, AR_ERR_UNSUPPORTED, "hidden %zu above 2^28", hidden);
     size_t bytes;
     if (!times(tokens, (size_t)topk, slots) || !times(hidden, *eb, row_bytes) ||
         !times(*slots, *row_bytes, &bytes))

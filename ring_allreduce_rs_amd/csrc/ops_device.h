@@ -183,6 +183,31 @@ __device__ __forceinline__ void st_place(char* row, Place p, u32x4 u) {
     }
 }
 
+// How the units of a row of n elements are loaded and stored: ROW_FULL where n
+// is a multiple of a unit, ROW_RAGGED where the last unit is a Place that moved
+// back, ROW_SHORT where a row is shorter than a unit.
+enum RowMode { ROW_FULL, ROW_RAGGED, ROW_SHORT };
+inline RowMode row_mode(size_t n, int eb) {
+    const size_t e = 16 / (size_t)eb;
+    return n % e == 0 ? ROW_FULL : n > e ? ROW_RAGGED : ROW_SHORT;
+}
+template <int EB, RowMode MODE>
+struct RowIO {
+    static constexpr int E = Vec<EB>::E;
+    __device__ __forceinline__ static Place place(unsigned unit, unsigned n) {
+        if constexpr (MODE == ROW_RAGGED) return place_unit<E>(unit * E, n);
+        else return Place{unit * E, 0};
+    }
+    __device__ __forceinline__ static u32x4 ld(const char* row, Place p, unsigned n) {
+        if constexpr (MODE == ROW_SHORT) return ld_unit_of<EB>(row, 0, n, 0u);
+        else return ld_unit<EB, true>(row + offset_here(p.at * EB));
+    }
+    __device__ __forceinline__ static void st(char* row, Place p, unsigned n, u32x4 u) {
+        if constexpr (MODE == ROW_SHORT) st_unit_of<EB>(row, 0, n, u);
+        else st_place<EB, MODE == ROW_RAGGED, true>(row, p, u);
+    }
+};
+
 // E parameters (weight, bias) at column i of n, `pb` bytes each; past the end
 // and for a NULL array they are `none`.
 template <int E>
@@ -230,6 +255,11 @@ __device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 // A value at a uniform address that no store of this kernel changes.
 __device__ __forceinline__ float ld_uniform(const float* p) {
     typedef const float __attribute__((address_space(4))) * constant_t;
+    return *(constant_t)(uintptr_t)p;
+}
+
+__device__ __forceinline__ int ld_uniform(const int* p) {
+    typedef const int __attribute__((address_space(4))) * constant_t;
     return *(constant_t)(uintptr_t)p;
 }
 

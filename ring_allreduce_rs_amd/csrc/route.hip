@@ -28,6 +28,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortSteps = 2;                            // slots per thread
 constexpr int kSortSlots = kSortThreads * kSortSteps;    // slots per block
+constexpr size_t kSortBlocks = 128;                      // at most
 constexpr int kMaxExperts = 1024;
 constexpr int kBins = kMaxExperts + 1;                   // the last one: no expert
 
@@ -68,7 +69,7 @@ __device__ __forceinline__ void wave_lds_order() {
 // Block b of the sort takes the slots [b * share, (b + 1) * share), in rounds
 // of kSortSlots; share is a multiple of that.
 
-// Slots per bin of each block's share.
+// Slots per bin of each block's share: work[bin][block].
 template <int IB>
 __global__ __launch_bounds__(kSortThreads) void k_route_count(const DispatchArgs a, size_t slots,
                                                               size_t share) {
@@ -80,8 +81,24 @@ __global__ __launch_bounds__(kSortThreads) void k_route_count(const DispatchArgs
     for (size_t i = begin + threadIdx.x; i < end; i += kSortThreads)
         atomicAdd(&cnt[bin_of<IB>(a.ids, i, a.experts)], 1);
     __syncthreads();
-    int* out = a.work + (size_t)blockIdx.x * (a.experts + 1);
-    for (int b = threadIdx.x; b <= a.experts; b += kSortThreads) out[b] = cnt[b];
+    for (int b = threadIdx.x; b <= a.experts; b += kSortThreads)
+        a.work[(size_t)b * gridDim.x + blockIdx.x] = cnt[b];
+}
+
+__device__ __forceinline__ int wave_total(int v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+// v becomes the sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d, 64);
+        if (lane >= d) v += o;
+    }
+    return v;
 }
 
 // Where each slot goes.  A block needs, for every bin, the slots in smaller
@@ -91,29 +108,43 @@ template <int IB>
 __global__ __launch_bounds__(kSortThreads) void k_route_place(const DispatchArgs a, size_t slots,
                                                               size_t share) {
     __shared__ int first[kBins];                       // next free row of each bin
+    __shared__ int total[kBins];
     __shared__ unsigned short wcnt[kSortWaves][kBins]; // slots per wavefront and bin
     __shared__ int wsum[kSortWaves];
     const int bins = a.experts + 1, bits = bin_bits(a.experts);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int nblk = slots ? (int)gridDim.x : 0;
+    const int nblk = gridDim.x, me = blockIdx.x;
 
-    // totals, and the part that earlier blocks hold
+    // a wavefront per bin: its slots in all blocks, and in the earlier ones;
+    // the loads of four bins are in flight together
+    constexpr int kAhead = 4;
+    static_assert(kSortBlocks <= 128, "a lane holds two blocks' counts");
+    for (int b0 = wave; b0 < bins; b0 += kSortWaves * kAhead) {
+        int lo[kAhead], hi[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int b = b0 + q * kSortWaves;
+            const int* w = a.work + (size_t)b * nblk;
+            lo[q] = b < bins && lane < nblk ? w[lane] : 0;
+            hi[q] = b < bins && lane + 64 < nblk ? w[lane + 64] : 0;
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int all = wave_total(lo[q] + hi[q]);
+            const int before = wave_total((lane < me ? lo[q] : 0) + (lane + 64 < me ? hi[q] : 0));
+            const int b = b0 + q * kSortWaves;
+            if (lane == 0 && b < bins) {
+                total[b] = all;
+                first[b] = before;
+            }
+        }
+    }
+    __syncthreads();
     int run = 0;
     for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
         const int b = b0 + (int)threadIdx.x;
-        int total = 0, before = 0;
-        if (b < bins)
-            for (int k = 0; k < nblk; ++k) {
-                const int c = a.work[(size_t)k * bins + b];
-                total += c;
-                if (k < (int)blockIdx.x) before += c;
-            }
-        int inc = total;   // inclusive sum over the wavefront
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(inc, d, 64);
-            if (lane >= d) inc += o;
-        }
+        const int mine = b < bins ? total[b] : 0;
+        const int inc = wave_scan(mine, lane);
         if (lane == 63) wsum[wave] = inc;
         __syncthreads();
         int ahead = run;
@@ -121,10 +152,9 @@ __global__ __launch_bounds__(kSortThreads) void k_route_place(const DispatchArgs
             if (w < wave) ahead += wsum[w];
             run += wsum[w];
         }
-        const int start = ahead + inc - total;
         if (b < bins) {
-            first[b] = start + before;
-            if (blockIdx.x == 0) a.offsets[b] = start;   // bin `experts`: the end of the last expert
+            first[b] += ahead + inc - mine;
+            if (me == 0) a.offsets[b] = ahead + inc - mine;   // bin `experts`: the last row in use
         }
         __syncthreads();
     }
@@ -183,109 +213,230 @@ __global__ __launch_bounds__(kSortThreads) void k_route_place(const DispatchArgs
 }
 
 // ------------------------------------------------------------------- moving rows
+//
+// A block of NT threads per token, so that what belongs to the token (its
+// sorted rows, its weights) is uniform: scalar registers hold the rows'
+// addresses, and the loads of KB choices are in flight together.
 
-constexpr int kRowThreads = 256;
-
-// A token's row to each of its sorted rows: TPT threads per token.
-template <int EB, int TPT>
-__global__ __launch_bounds__(kRowThreads) void k_route_rows(const DispatchArgs a) {
-    constexpr int E = Vec<EB>::E;
-    const size_t n = (size_t)a.tokens * a.topk;
-    const int live = a.offsets[a.experts];
-    for (size_t t = (size_t)blockIdx.x * (kRowThreads / TPT) + threadIdx.x / TPT;
-         t < (size_t)a.tokens; t += (size_t)gridDim.x * (kRowThreads / TPT)) {
+// A token's row to each of its sorted rows.
+template <int EB, int NT, RowMode MODE>
+__global__ __launch_bounds__(NT) void k_route_rows(const DispatchArgs a) {
+    const int live = ld_uniform(a.offsets + a.experts);
+    for (size_t t = blockIdx.x; t < (size_t)a.tokens; t += gridDim.x) {
         const char* x = static_cast<const char*>(a.x) + t * a.xstride * EB;
-        const int* dest = a.dest + t * a.topk;
-        for (size_t i = (size_t)(threadIdx.x % TPT) * E; i < a.hidden; i += (size_t)TPT * E) {
-            const u32x4 u = ld_unit_of<EB>(x, i, a.hidden, 0u);
+        using IO = RowIO<EB, MODE>;
+        const unsigned hidden = (unsigned)a.hidden, units = (hidden + IO::E - 1) / IO::E;
+        const size_t n = (size_t)a.tokens * a.topk;
+        for (unsigned i = threadIdx.x; i < units; i += NT) {
+            const Place p = IO::place(i, hidden);
+            const u32x4 u = IO::ld(x, p, hidden);
+            const u32x4 z = {0u, 0u, 0u, 0u};
             for (int k = 0; k < a.topk; ++k) {
-                const int d = dest[k];
+                const int d = ld_uniform(a.dest + t * a.topk + k);
                 if ((size_t)d >= n) continue;
-                const u32x4 z = {0u, 0u, 0u, 0u};
-                st_unit_of<EB>(static_cast<char*>(a.rows) + (size_t)d * a.hidden * EB, i, a.hidden,
-                               d < live ? u : z);
+                IO::st(static_cast<char*>(a.rows) + (size_t)d * a.hidden * EB, p, hidden,
+                       d < live ? u : z);
             }
+        }
+    }
+}
+
+// The whole dispatch in one launch, for few slots: the last block counts the
+// experts' rows, every other block finds where its token's choices go by
+// comparing them with every slot, then copies.  (From kDirectSlots slots on the
+// comparisons cost more than the sort's launches.)
+template <int EB, int IB, int NT, RowMode MODE>
+__global__ __launch_bounds__(NT) void k_route_direct(const DispatchArgs a, int slots) {
+    constexpr int W = NT / 64, KB = 8;
+    __shared__ int lds[2][W * KB];
+    __shared__ int cnt[kBins];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if ((int)blockIdx.x == a.tokens) {
+        for (int b = threadIdx.x; b <= a.experts; b += NT) cnt[b] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < slots; i += NT)
+            atomicAdd(&cnt[bin_of<IB>(a.ids, i, a.experts)], 1);
+        __syncthreads();
+        if (wave == 0) {
+            int run = 0;
+            for (int b0 = 0; b0 <= a.experts; b0 += 64) {
+                const int mine = b0 + lane <= a.experts ? cnt[b0 + lane] : 0;
+                const int inc = wave_scan(mine, lane);
+                if (b0 + lane <= a.experts) a.offsets[b0 + lane] = run + inc - mine;
+                run += __builtin_amdgcn_readlane(inc, 63);
+            }
+        }
+        return;
+    }
+    const size_t t = blockIdx.x;
+    using IO = RowIO<EB, MODE>;
+    const unsigned hidden = (unsigned)a.hidden, units = (hidden + IO::E - 1) / IO::E;
+    const char* x = static_cast<const char*>(a.x) + t * a.xstride * EB;
+    int buf = 0;
+    for (int k0 = 0; k0 < a.topk; k0 += KB, buf ^= 1) {
+        const int i0 = (int)t * a.topk + k0;
+        int bin[KB], before[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            bin[k] = k0 + k < a.topk ? bin_of<IB>(a.ids, i0 + k, a.experts) : -1;
+            before[k] = 0;
+        }
+        for (int i = threadIdx.x; i < slots; i += NT) {
+            const int e = bin_of<IB>(a.ids, i, a.experts);
+#pragma unroll
+            for (int k = 0; k < KB; ++k) before[k] += e < bin[k] || (e == bin[k] && i < i0 + k);
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            before[k] = wave_total(before[k]);
+            if (W > 1 && lane == 0) lds[buf][wave * KB + k] = before[k];
+        }
+        if constexpr (W > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                before[k] = 0;
+#pragma unroll
+                for (int w = 0; w < W; ++w) before[k] += lds[buf][w * KB + k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+            if (threadIdx.x == 0 && k0 + k < a.topk) {
+                a.dest[i0 + k] = before[k];
+                a.slot[before[k]] = i0 + k;
+            }
+        for (unsigned i = threadIdx.x; i < units; i += NT) {
+            const Place p = IO::place(i, hidden);
+            const u32x4 u = IO::ld(x, p, hidden), z = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+                if (k0 + k < a.topk)
+                    IO::st(static_cast<char*>(a.rows) + (size_t)before[k] * a.hidden * EB, p, hidden,
+                           bin[k] < a.experts ? u : z);
         }
     }
 }
 
 // y[t] = sum_k w[t,k] rows[dest[t,k]]
-template <int EB, int TPT>
-__global__ __launch_bounds__(kRowThreads) void k_route_combine(const CombineArgs a) {
-    constexpr int E = Vec<EB>::E;
+template <int EB, int NT, int KB, RowMode MODE>
+__global__ __launch_bounds__(NT) void k_route_combine(const CombineArgs a) {
+    using IO = RowIO<EB, MODE>;
+    constexpr int E = IO::E;
+    const unsigned hidden = (unsigned)a.hidden, units = (hidden + E - 1) / E;
     const int n = a.tokens * a.topk;
-    const int live = min(a.offsets[a.experts], n);
-    for (size_t t = (size_t)blockIdx.x * (kRowThreads / TPT) + threadIdx.x / TPT;
-         t < (size_t)a.tokens; t += (size_t)gridDim.x * (kRowThreads / TPT)) {
-        const int* dest = a.dest + t * a.topk;
-        const float* w = a.weights ? a.weights + t * a.topk : nullptr;
+    const int live = min(ld_uniform(a.offsets + a.experts), n);
+    for (size_t t = blockIdx.x; t < (size_t)a.tokens; t += gridDim.x) {
         char* y = static_cast<char*>(a.y) + t * a.hidden * EB;
-        for (size_t i = (size_t)(threadIdx.x % TPT) * E; i < a.hidden; i += (size_t)TPT * E) {
+        for (unsigned i = threadIdx.x; i < units; i += NT) {
+            const Place p = IO::place(i, hidden);
             float acc[E] = {};
-            for (int k = 0; k < a.topk; ++k) {
-                const int d = dest[k];
-                if (d < 0 || d >= live) continue;
-                const float wk = w ? w[k] : 1.0f;
-                float v[E];
-                Vec<EB>::unpack(ld_unit_of<EB>(static_cast<const char*>(a.rows) +
-                                                   (size_t)d * a.hidden * EB, i, a.hidden, 0u), v);
+            for (int k0 = 0; k0 < a.topk; k0 += KB) {
+                u32x4 raw[KB];
+                float w[KB];
 #pragma unroll
-                for (int j = 0; j < E; ++j) acc[j] = __builtin_fmaf(v[j], wk, acc[j]);
-            }
-            st_unit_of<EB>(y, i, a.hidden, Vec<EB>::pack(acc));
-        }
-    }
-}
-
-// drows and dweights: a wavefront per token, one choice at a time.
-template <int EB>
-__global__ __launch_bounds__(kRowThreads) void k_route_combine_grad(const CombineArgs a) {
-    constexpr int E = Vec<EB>::E;
-    const int n = a.tokens * a.topk;
-    const int live = min(a.offsets[a.experts], n);
-    const int lane = threadIdx.x & 63;
-    for (size_t t = (size_t)blockIdx.x * (kRowThreads / 64) + threadIdx.x / 64;
-         t < (size_t)a.tokens; t += (size_t)gridDim.x * (kRowThreads / 64)) {
-        const char* dy = static_cast<const char*>(a.dy) + t * a.dystride * EB;
-        for (int k = 0; k < a.topk; ++k) {
-            const int d = a.dest[t * a.topk + k];
-            const bool ok = d >= 0 && d < live;
-            const float wk = a.weights[t * a.topk + k];
-            float dot = 0.0f;
-            if (d >= 0 && d < n) {
-                const char* row = static_cast<const char*>(a.rows) + (size_t)d * a.hidden * EB;
-                char* drow = static_cast<char*>(a.drows) + (size_t)d * a.hidden * EB;
-                for (size_t i = (size_t)lane * E; i < a.hidden; i += 64 * E) {
-                    u32x4 out = {0u, 0u, 0u, 0u};
-                    if (ok) {
-                        float g[E], v[E];
-                        Vec<EB>::unpack(ld_unit_of<EB>(dy, i, a.hidden, 0u), g);
-                        Vec<EB>::unpack(ld_unit_of<EB>(row, i, a.hidden, 0u), v);
-#pragma unroll
-                        for (int j = 0; j < E; ++j) {
-                            dot = __builtin_fmaf(g[j], v[j], dot);
-                            g[j] *= wk;
-                        }
-                        out = Vec<EB>::pack(g);
+                for (int k = 0; k < KB; ++k) {
+                    const size_t s = t * a.topk + k0 + k;
+                    const int d = k0 + k < a.topk ? ld_uniform(a.dest + s) : -1;
+                    raw[k] = u32x4{0u, 0u, 0u, 0u};
+                    w[k] = 0.0f;
+                    if (d >= 0 && d < live) {   // (the same for the whole block)
+                        raw[k] = IO::ld(static_cast<const char*>(a.rows) +
+                                            (size_t)d * a.hidden * EB, p, hidden);
+                        w[k] = a.weights ? ld_uniform(a.weights + s) : 1.0f;
                     }
-                    st_unit_of<EB>(drow, i, a.hidden, out);
+                }
+#pragma unroll
+                for (int k = 0; k < KB; ++k) {
+                    float v[E];
+                    Vec<EB>::unpack(raw[k], v);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) acc[j] = __builtin_fmaf(v[j], w[k], acc[j]);
                 }
             }
-            dot = wave_sum(dot);
-            if (lane == 0) a.dweights[t * a.topk + k] = ok ? dot : 0.0f;
+            IO::st(y, p, hidden, Vec<EB>::pack(acc));
         }
     }
 }
 
-unsigned token_blocks(int tokens, int per) {
-    constexpr int kMost = 1 << 22;
-    const int b = tokens / per + (tokens % per != 0);
-    return (unsigned)(b < 1 ? 1 : b < kMost ? b : kMost);
+// drows and dweights: the token's gradient is read once for KB choices.
+template <int EB, int NT, int KB, RowMode MODE>
+__global__ __launch_bounds__(NT) void k_route_combine_grad(const CombineArgs a) {
+    using IO = RowIO<EB, MODE>;
+    constexpr int E = IO::E, W = NT / 64;
+    __shared__ float lds[2][W * KB];
+    const unsigned hidden = (unsigned)a.hidden, units = (hidden + E - 1) / E;
+    const int n = a.tokens * a.topk;
+    const int live = min(ld_uniform(a.offsets + a.experts), n);
+    int buf = 0;
+    for (size_t t = blockIdx.x; t < (size_t)a.tokens; t += gridDim.x) {
+        const char* dy = static_cast<const char*>(a.dy) + t * a.dystride * EB;
+        for (int k0 = 0; k0 < a.topk; k0 += KB, buf ^= 1) {
+            float dot[KB];
+#pragma unroll
+            for (int k = 0; k < KB; ++k) dot[k] = 0.0f;
+            for (unsigned i = threadIdx.x; i < units; i += NT) {
+                const Place p = IO::place(i, hidden);
+                u32x4 raw[KB], rg = IO::ld(dy, p, hidden);
+#pragma unroll
+                for (int k = 0; k < KB; ++k) {
+                    const int d = k0 + k < a.topk ? ld_uniform(a.dest + t * a.topk + k0 + k) : -1;
+                    raw[k] = u32x4{0u, 0u, 0u, 0u};
+                    if (d >= 0 && d < live)
+                        raw[k] = IO::ld(static_cast<const char*>(a.rows) +
+                                            (size_t)d * a.hidden * EB, p, hidden);
+                }
+                if (MODE == ROW_RAGGED && p.skip) rg = drop_first<EB, true>(rg, p.skip);
+                float g[E];
+                Vec<EB>::unpack(rg, g);
+#pragma unroll
+                for (int k = 0; k < KB; ++k) {
+                    const size_t s = t * a.topk + k0 + k;
+                    const int d = k0 + k < a.topk ? ld_uniform(a.dest + s) : -1;
+                    if (d < 0 || d >= n) continue;
+                    u32x4 out = {0u, 0u, 0u, 0u};
+                    if (d < live) {
+                        const float w = ld_uniform(a.weights + s);
+                        float v[E];
+                        Vec<EB>::unpack(raw[k], v);
+#pragma unroll
+                        for (int j = 0; j < E; ++j) {
+                            dot[k] = __builtin_fmaf(g[j], v[j], dot[k]);
+                            v[j] = g[j] * w;
+                        }
+                        out = Vec<EB>::pack(v);
+                    }
+                    IO::st(static_cast<char*>(a.drows) + (size_t)d * a.hidden * EB, p, hidden, out);
+                }
+            }
+            block_sums<W, KB>(dot, lds[buf]);
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+                if (threadIdx.x == 0 && k0 + k < a.topk) {
+                    const size_t s = t * a.topk + k0 + k;
+                    const int d = a.dest[s];
+                    a.dweights[s] = d >= 0 && d < live ? dot[k] : 0.0f;
+                }
+        }
+    }
 }
+
+// Blocks of a launch over tokens (the kernels walk the rest).
+unsigned token_blocks(int tokens) {
+    constexpr int kMost = 1 << 22;
+    return (unsigned)(tokens < kMost ? tokens : kMost);
+}
+
+// Threads of a token's block: a row's units, at most 256.
+int token_threads(size_t hidden, int eb) {
+    const size_t units = (hidden * eb + 15) / 16;
+    return units <= 64 ? 64 : units <= 128 ? 128 : 256;
+}
+
+constexpr size_t kDirectSlots = 2048;
 
 // The sort's split: as many blocks as there are kSortSlots, at most kSortBlocks
 // (each block adds up the counts of all of them).
-constexpr size_t kSortBlocks = 128;
 size_t sort_share(size_t slots) {
     const size_t rounds = (slots + kSortSlots - 1) / kSortSlots;
     const size_t each = (rounds + kSortBlocks - 1) / kSortBlocks;
@@ -297,62 +448,88 @@ int sort_blocks(size_t slots) {
     return b ? (int)b : 1;
 }
 
-template <int EB>
-hipError_t rows_by_width(const DispatchArgs& a, hipStream_t s) {
-    const size_t units = (a.hidden * EB + 15) / 16;
-    if (units <= 64)
-        hipLaunchKernelGGL((k_route_rows<EB, 64>), dim3(token_blocks(a.tokens, kRowThreads / 64)),
-                           dim3(kRowThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_route_rows<EB, 256>), dim3(token_blocks(a.tokens, 1)),
-                           dim3(kRowThreads), 0, s, a);
-    return hipGetLastError();
-}
-
-template <int EB>
-hipError_t combine_by_width(const CombineArgs& a, hipStream_t s) {
-    const size_t units = (a.hidden * EB + 15) / 16;
-    if (units <= 64)
-        hipLaunchKernelGGL((k_route_combine<EB, 64>), dim3(token_blocks(a.tokens, kRowThreads / 64)),
-                           dim3(kRowThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_route_combine<EB, 256>), dim3(token_blocks(a.tokens, 1)),
-                           dim3(kRowThreads), 0, s, a);
-    return hipGetLastError();
-}
+// CALL(EB, NT, MODE) with the types and sizes of `a`.
+#define BY_MODE(EB, NT, CALL)                              \
+    do {                                                   \
+        if (mode == ROW_FULL) { CALL(EB, NT, ROW_FULL); }  \
+        else if (mode == ROW_RAGGED) { CALL(EB, NT, ROW_RAGGED); } \
+        else { CALL(EB, NT, ROW_SHORT); }                  \
+    } while (0)
+#define BY_WIDTH(EB, CALL)                  \
+    do {                                    \
+        if (nt == 64) BY_MODE(EB, 64, CALL); \
+        else if (nt == 128) BY_MODE(EB, 128, CALL); \
+        else BY_MODE(EB, 256, CALL);        \
+    } while (0)
+#define BY_ROW(CALL)                                        \
+    do {                                                    \
+        const int nt = token_threads(a.hidden, a.eb);       \
+        const RowMode mode = row_mode(a.hidden, a.eb);      \
+        if (a.eb == 2) BY_WIDTH(2, CALL);                   \
+        else BY_WIDTH(4, CALL);                             \
+    } while (0)
 
 }  // namespace
 
 size_t dispatch_work_ints(size_t slots, int experts) {
+    if (slots <= kDirectSlots) return 0;
     return (size_t)sort_blocks(slots) * (size_t)(experts + 1);
 }
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
-    const size_t slots = (size_t)a.tokens * a.topk, share = sort_share(slots);
-    const dim3 grid(sort_blocks(slots)), block(kSortThreads);
-    if (slots > 0) {
-        if (a.ib == 8) hipLaunchKernelGGL(k_route_count<8>, grid, block, 0, s, a, slots, share);
-        else hipLaunchKernelGGL(k_route_count<4>, grid, block, 0, s, a, slots, share);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    const size_t slots = (size_t)a.tokens * a.topk;
+    if (slots <= kDirectSlots) {
+        const dim3 grid(a.tokens + 1);
+#define CALL(EB, NT, MODE)                                                                    \
+    if (a.ib == 8)                                                                            \
+        hipLaunchKernelGGL((k_route_direct<EB, 8, NT, MODE>), grid, dim3(NT), 0, s, a, (int)slots); \
+    else                                                                                      \
+        hipLaunchKernelGGL((k_route_direct<EB, 4, NT, MODE>), grid, dim3(NT), 0, s, a, (int)slots)
+        BY_ROW(CALL);
+#undef CALL
+        return hipGetLastError();
     }
+    const size_t share = sort_share(slots);
+    const dim3 grid(sort_blocks(slots)), block(kSortThreads);
+    if (a.ib == 8) hipLaunchKernelGGL(k_route_count<8>, grid, block, 0, s, a, slots, share);
+    else hipLaunchKernelGGL(k_route_count<4>, grid, block, 0, s, a, slots, share);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     if (a.ib == 8) hipLaunchKernelGGL(k_route_place<8>, grid, block, 0, s, a, slots, share);
     else hipLaunchKernelGGL(k_route_place<4>, grid, block, 0, s, a, slots, share);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || slots == 0) return e;
-    return a.eb == 2 ? rows_by_width<2>(a, s) : rows_by_width<4>(a, s);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+#define CALL(EB, NT, MODE)                                                                  \
+    hipLaunchKernelGGL((k_route_rows<EB, NT, MODE>), dim3(token_blocks(a.tokens)), dim3(NT), 0, s, a)
+    BY_ROW(CALL);
+#undef CALL
+    return hipGetLastError();
 }
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;
-    return a.eb == 2 ? combine_by_width<2>(a, s) : combine_by_width<4>(a, s);
+    const dim3 grid(token_blocks(a.tokens));
+#define CALL(EB, NT, MODE)                                                                        \
+    if (a.topk <= 2) hipLaunchKernelGGL((k_route_combine<EB, NT, 2, MODE>), grid, dim3(NT), 0, s, a); \
+    else if (a.topk <= 4)                                                                         \
+        hipLaunchKernelGGL((k_route_combine<EB, NT, 4, MODE>), grid, dim3(NT), 0, s, a);          \
+    else hipLaunchKernelGGL((k_route_combine<EB, NT, 8, MODE>), grid, dim3(NT), 0, s, a)
+    BY_ROW(CALL);
+#undef CALL
+    return hipGetLastError();
 }
 
 hipError_t launch_combine_grad(const CombineArgs& a, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;
-    const dim3 grid(token_blocks(a.tokens, kRowThreads / 64)), block(kRowThreads);
-    if (a.eb == 2) hipLaunchKernelGGL(k_route_combine_grad<2>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_route_combine_grad<4>, grid, block, 0, s, a);
+    const dim3 grid(token_blocks(a.tokens));
+#define CALL(EB, NT, MODE)                                                                    \
+    if (a.topk <= 2)                                                                          \
+        hipLaunchKernelGGL((k_route_combine_grad<EB, NT, 2, MODE>), grid, dim3(NT), 0, s, a); \
+    else if (a.topk <= 4)                                                                     \
+        hipLaunchKernelGGL((k_route_combine_grad<EB, NT, 4, MODE>), grid, dim3(NT), 0, s, a); \
+    else hipLaunchKernelGGL((k_route_combine_grad<EB, NT, 8, MODE>), grid, dim3(NT), 0, s, a)
+    BY_ROW(CALL);
+#undef CALL
     return hipGetLastError();
 }
 

@@ -140,6 +140,7 @@ void route() {
     REFUSED(AR_ERR_INVALID_ARG, d(at(0), 16, 8, 10, 2, 5, 16, AR_FLOAT32, at<int>(3), at(6), need));
     REFUSED(AR_ERR_INVALID_ARG, d(at(0), 16, 8, 10, 2, 5, 16, AR_FLOAT32, at<int>(4), at(6), need - 1));
     REFUSED(AR_ERR_UNSUPPORTED, d(at(0), 16, 8, 10, 2, 1025, 16, AR_FLOAT32, at<int>(4), at(6), need));
+    REFUSED(AR_ERR_UNSUPPORTED, d(at(0), size_t(1) << 29, 8, 1, 2, 5, (size_t(1) << 28) + 1, AR_FLOAT32, at<int>(4), at(6), need));
     REFUSED(AR_ERR_UNSUPPORTED, d(at(0), 1, 8, size_t(1) << 31, 1, 5, 1, AR_FLOAT32, at<int>(4), at(6), need));
     REFUSED(AR_ERR_INVALID_ARG, d(at(0), 16, 8, SIZE_MAX / 2, 2, 5, 16, AR_FLOAT32, at<int>(4), at(6), need));
 
