@@ -48,7 +48,7 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
             const char* x = static_cast<const char*>(a.x) + r * a.xstride * EB;
 #pragma unroll
             for (int u = 0; u < UPT; ++u)
-                raw[k][u] = ld_unit<EB, true>(x + offset_here(at[u].at * EB));
+                raw[k][u] = ld_unit<EB>(x + offset_here(at[u].at * EB));
         }
         float mean[R], s[R];
 #pragma unroll
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
                     const float xh = (v[j] - mean[k]) * rstd[k];
                     v[j] = rstd[k] * __builtin_fmaf(-xh, c2, __builtin_fmaf(g[j], w[u][j], -c1));
                 }
-                st_place<EB, RAGGED, true>(dx, at[u], Vec<EB>::pack(v));
+                st_place<EB, RAGGED>(dx, at[u], Vec<EB>::pack(v));
             }
             __builtin_amdgcn_sched_barrier(0);
         }

@@ -191,7 +191,9 @@ inline RowMode row_mode(size_t n, int eb) {
     const size_t e = 16 / (size_t)eb;
     return n % e == 0 ? ROW_FULL : n > e ? ROW_RAGGED : ROW_SHORT;
 }
-template <int EB, RowMode MODE>
+// NT: the loads bypass the caches, for rows that are read once and would only
+// push other data out.
+template <int EB, RowMode MODE, bool NT>
 struct RowIO {
     static constexpr int E = Vec<EB>::E;
     __device__ __forceinline__ static Place place(unsigned unit, unsigned n) {
@@ -200,7 +202,7 @@ struct RowIO {
     }
     __device__ __forceinline__ static u32x4 ld(const char* row, Place p, unsigned n) {
         if constexpr (MODE == ROW_SHORT) return ld_unit_of<EB>(row, 0, n, 0u);
-        else return ld_unit<EB, true>(row + offset_here(p.at * EB));
+        else return ld_unit<EB, NT>(row + offset_here(p.at * EB));
     }
     __device__ __forceinline__ static void st(char* row, Place p, unsigned n, u32x4 u) {
         if constexpr (MODE == ROW_SHORT) st_unit_of<EB>(row, 0, n, u);
@@ -290,6 +292,18 @@ __device__ __forceinline__ float wave_sum(float v) {
     v += dpp<kDppLast15, 0xa>(0.0f, v);   // rows 1 and 3
     v += dpp<kDppLast31, 0xc>(0.0f, v);   // rows 2 and 3
     return lane63(v);
+}
+
+__device__ __forceinline__ int wave_sum(int v) {
+#define ADD(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false)
+    ADD(kDppSwap1, 0xf);
+    ADD(kDppSwap2, 0xf);
+    ADD(kDppHalfMirror, 0xf);
+    ADD(kDppMirror, 0xf);
+    ADD(kDppLast15, 0xa);
+    ADD(kDppLast31, 0xc);
+#undef ADD
+    return __builtin_amdgcn_readlane(v, 63);
 }
 
 __device__ __forceinline__ float wave_max(float v) {

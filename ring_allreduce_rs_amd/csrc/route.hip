@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortSteps = 2;                            // slots per thread
+constexpr int kSortSteps = 1;                            // slots per thread
 constexpr int kSortSlots = kSortThreads * kSortSteps;    // slots per block
 constexpr size_t kSortBlocks = 128;                      // at most
 constexpr int kMaxExperts = 1024;
@@ -85,12 +85,6 @@ __global__ __launch_bounds__(kSortThreads) void k_route_count(const DispatchArgs
         a.work[(size_t)b * gridDim.x + blockIdx.x] = cnt[b];
 }
 
-__device__ __forceinline__ int wave_total(int v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
-}
-
 // v becomes the sum over the lanes up to this one.
 __device__ __forceinline__ int wave_scan(int v, int lane) {
 #pragma unroll
@@ -115,9 +109,23 @@ __global__ __launch_bounds__(kSortThreads) void k_route_place(const DispatchArgs
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int nblk = gridDim.x, me = blockIdx.x;
 
+    // the first round's slots (wavefront w takes 64 * kSortSteps in a row) are
+    // loaded before the counts that they wait for
+    const size_t begin = (size_t)me * share;
+    const size_t own = (size_t)(wave * kSortSteps) * 64 + lane;
+    int bin[kSortSteps];
+    const auto load_bins = [&](size_t round) {
+#pragma unroll
+        for (int s = 0; s < kSortSteps; ++s) {
+            const size_t i = round + own + s * 64;
+            bin[s] = i < slots ? bin_of<IB>(a.ids, i, a.experts) : 0;
+        }
+    };
+    load_bins(begin);
+
     // a wavefront per bin: its slots in all blocks, and in the earlier ones;
-    // the loads of four bins are in flight together
-    constexpr int kAhead = 4;
+    // the loads of kAhead bins are in flight together
+    constexpr int kAhead = 12;
     static_assert(kSortBlocks <= 128, "a lane holds two blocks' counts");
     for (int b0 = wave; b0 < bins; b0 += kSortWaves * kAhead) {
         int lo[kAhead], hi[kAhead];
@@ -130,8 +138,8 @@ __global__ __launch_bounds__(kSortThreads) void k_route_place(const DispatchArgs
         }
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            const int all = wave_total(lo[q] + hi[q]);
-            const int before = wave_total((lane < me ? lo[q] : 0) + (lane + 64 < me ? hi[q] : 0));
+            const int all = wave_sum(lo[q] + hi[q]);
+            const int before = wave_sum((lane < me ? lo[q] : 0) + (lane + 64 < me ? hi[q] : 0));
             const int b = b0 + q * kSortWaves;
             if (lane == 0 && b < bins) {
                 total[b] = all;
@@ -159,18 +167,14 @@ __global__ __launch_bounds__(kSortThreads) void k_route_place(const DispatchArgs
         __syncthreads();
     }
 
-    const size_t begin = blockIdx.x * share;
     for (size_t round = begin; round < begin + share && round < slots; round += kSortSlots) {
-        // wavefront w takes 64 * kSortSteps slots in a row
-        const size_t base = round + wave * 64 * kSortSteps;
+        if (round != begin) load_bins(round);
         for (int b = lane; b < bins; b += 64) wcnt[wave][b] = 0;
         wave_lds_order();
-        int bin[kSortSteps], rank[kSortSteps];
+        int rank[kSortSteps];
 #pragma unroll
         for (int s = 0; s < kSortSteps; ++s) {
-            const size_t i = base + s * 64 + lane;
-            const bool live = i < slots;
-            bin[s] = live ? bin_of<IB>(a.ids, i, a.experts) : 0;
+            const bool live = round + own + s * 64 < slots;
             const unsigned long long m = same_bin(bin[s], bits, live);
             const int below = __popcll(m & ((1ull << lane) - 1));
             const int had = wcnt[wave][bin[s]];
@@ -186,17 +190,21 @@ __global__ __launch_bounds__(kSortThreads) void k_route_place(const DispatchArgs
         for (int q = 0; q < (kBins + kSortThreads - 1) / kSortThreads; ++q) {
             const int b = q * kSortThreads + (int)threadIdx.x;
             sum[q] = 0;
-            if (b < bins)
+            if (b < bins) {
+                int c[kSortWaves];
+#pragma unroll
+                for (int w = 0; w < kSortWaves; ++w) c[w] = wcnt[w][b];
+#pragma unroll
                 for (int w = 0; w < kSortWaves; ++w) {
-                    const int c = wcnt[w][b];
                     wcnt[w][b] = (unsigned short)sum[q];
-                    sum[q] += c;
+                    sum[q] += c[w];
                 }
+            }
         }
         __syncthreads();
 #pragma unroll
         for (int s = 0; s < kSortSteps; ++s) {
-            const size_t i = base + s * 64 + lane;
+            const size_t i = round + own + s * 64;
             if (i >= slots) continue;
             const int d = first[bin[s]] + wcnt[wave][bin[s]] + rank[s];
             a.dest[i] = d;
@@ -224,7 +232,7 @@ __global__ __launch_bounds__(NT) void k_route_rows(const DispatchArgs a) {
     const int live = ld_uniform(a.offsets + a.experts);
     for (size_t t = blockIdx.x; t < (size_t)a.tokens; t += gridDim.x) {
         const char* x = static_cast<const char*>(a.x) + t * a.xstride * EB;
-        using IO = RowIO<EB, MODE>;
+        using IO = RowIO<EB, MODE, false>;
         const unsigned hidden = (unsigned)a.hidden, units = (hidden + IO::E - 1) / IO::E;
         const size_t n = (size_t)a.tokens * a.topk;
         for (unsigned i = threadIdx.x; i < units; i += NT) {
@@ -269,9 +277,12 @@ __global__ __launch_bounds__(NT) void k_route_direct(const DispatchArgs a, int s
         return;
     }
     const size_t t = blockIdx.x;
-    using IO = RowIO<EB, MODE>;
+    using IO = RowIO<EB, MODE, false>;
     const unsigned hidden = (unsigned)a.hidden, units = (hidden + IO::E - 1) / IO::E;
     const char* x = static_cast<const char*>(a.x) + t * a.xstride * EB;
+    // the row's first units come while the slots are compared
+    const Place mine = IO::place(threadIdx.x < units ? threadIdx.x : 0, hidden);
+    const u32x4 held = IO::ld(x, mine, hidden);
     int buf = 0;
     for (int k0 = 0; k0 < a.topk; k0 += KB, buf ^= 1) {
         const int i0 = (int)t * a.topk + k0;
@@ -288,7 +299,7 @@ __global__ __launch_bounds__(NT) void k_route_direct(const DispatchArgs a, int s
         }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-            before[k] = wave_total(before[k]);
+            before[k] = wave_sum(before[k]);
             if (W > 1 && lane == 0) lds[buf][wave * KB + k] = before[k];
         }
         if constexpr (W > 1) {
@@ -308,7 +319,7 @@ __global__ __launch_bounds__(NT) void k_route_direct(const DispatchArgs a, int s
             }
         for (unsigned i = threadIdx.x; i < units; i += NT) {
             const Place p = IO::place(i, hidden);
-            const u32x4 u = IO::ld(x, p, hidden), z = {0u, 0u, 0u, 0u};
+            const u32x4 u = i < NT ? held : IO::ld(x, p, hidden), z = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int k = 0; k < KB; ++k)
                 if (k0 + k < a.topk)
@@ -319,9 +330,9 @@ __global__ __launch_bounds__(NT) void k_route_direct(const DispatchArgs a, int s
 }
 
 // y[t] = sum_k w[t,k] rows[dest[t,k]]
-template <int EB, int NT, int KB, RowMode MODE>
+template <int EB, int NT, int KB, RowMode MODE, bool STREAM>
 __global__ __launch_bounds__(NT) void k_route_combine(const CombineArgs a) {
-    using IO = RowIO<EB, MODE>;
+    using IO = RowIO<EB, MODE, STREAM>;
     constexpr int E = IO::E;
     const unsigned hidden = (unsigned)a.hidden, units = (hidden + E - 1) / E;
     const int n = a.tokens * a.topk;
@@ -362,7 +373,7 @@ __global__ __launch_bounds__(NT) void k_route_combine(const CombineArgs a) {
 // drows and dweights: the token's gradient is read once for KB choices.
 template <int EB, int NT, int KB, RowMode MODE>
 __global__ __launch_bounds__(NT) void k_route_combine_grad(const CombineArgs a) {
-    using IO = RowIO<EB, MODE>;
+    using IO = RowIO<EB, MODE, true>;
     constexpr int E = IO::E, W = NT / 64;
     __shared__ float lds[2][W * KB];
     const unsigned hidden = (unsigned)a.hidden, units = (hidden + E - 1) / E;
@@ -434,6 +445,12 @@ int token_threads(size_t hidden, int eb) {
 }
 
 constexpr size_t kDirectSlots = 2048;
+
+// Rows of more bytes than this are read past the caches on the way back: they
+// would only push each other out of the 256 MB last-level cache (MI355X, rows
+// of 537 MB: 98 us against 106; rows of 98 MB that are still in it: 19.5 us
+// past it, 16.9 through it).
+constexpr size_t kStreamBytes = size_t(192) << 20;
 
 // The sort's split: as many blocks as there are kSortSlots, at most kSortBlocks
 // (each block adds up the counts of all of them).
@@ -509,13 +526,18 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;
     const dim3 grid(token_blocks(a.tokens));
-#define CALL(EB, NT, MODE)                                                                        \
-    if (a.topk <= 2) hipLaunchKernelGGL((k_route_combine<EB, NT, 2, MODE>), grid, dim3(NT), 0, s, a); \
-    else if (a.topk <= 4)                                                                         \
-        hipLaunchKernelGGL((k_route_combine<EB, NT, 4, MODE>), grid, dim3(NT), 0, s, a);          \
-    else hipLaunchKernelGGL((k_route_combine<EB, NT, 8, MODE>), grid, dim3(NT), 0, s, a)
+    const bool stream = (size_t)a.tokens * a.topk * a.hidden * a.eb > kStreamBytes;
+#define CALL2(EB, NT, KB, MODE)                                                                    \
+    if (stream)                                                                                    \
+        hipLaunchKernelGGL((k_route_combine<EB, NT, KB, MODE, true>), grid, dim3(NT), 0, s, a);    \
+    else hipLaunchKernelGGL((k_route_combine<EB, NT, KB, MODE, false>), grid, dim3(NT), 0, s, a)
+#define CALL(EB, NT, MODE)                              \
+    if (a.topk <= 2) { CALL2(EB, NT, 2, MODE); }        \
+    else if (a.topk <= 4) { CALL2(EB, NT, 4, MODE); }   \
+    else { CALL2(EB, NT, 8, MODE); }
     BY_ROW(CALL);
 #undef CALL
+#undef CALL2
     return hipGetLastError();
 }
 
