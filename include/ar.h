@@ -527,7 +527,7 @@ ar_status ar_expert_combine_backward(ar_ctx* ctx, const void* dy, size_t dy_stri
  * An entry with p == 0 adds nothing; a place named twice counts twice; a row
  * that keeps no entry (or whose kept teacher logits are all -inf) has loss 0.
  * loss and lse: binary32, rows.  teacher has the logits' dtype.  Limits
- * (AR_ERR_UNSUPPORTED): top <= AR_DISTILL_MAX_TOP, vocab <= 2^31 - 1.
+ * (AR_ERR_UNSUPPORTED): top <= AR_DISTILL_MAX_TOP, vocab <= 2^28.
  * vocab and top > 0; rows == 0 is a successful no-op. */
 #define AR_DISTILL_MAX_TOP 1024
 ar_status ar_distill_loss(ar_ctx* ctx, const void* logits, size_t logits_stride,

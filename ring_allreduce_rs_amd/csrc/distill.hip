@@ -88,10 +88,10 @@ __device__ bool load_teacher(const DistillArgs& a, size_t r, Teacher& th, float*
     return !(s == 0.0f);
 }
 
-// The row's loss, on every thread.
+// The row's loss, on every thread, with log q = (z - base) / T - logz.
 template <int EB, int IB, int W>
 __device__ float row_loss(const DistillArgs& a, size_t r, Teacher& th, float zmax, float logs,
-                          float lse) {
+                          float base, float logz) {
     const char* t = static_cast<const char*>(a.teacher) + r * a.top * EB;
     const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
     float s = 0.0f;
@@ -99,7 +99,8 @@ __device__ float row_loss(const DistillArgs& a, size_t r, Teacher& th, float zma
         const float p = th.p[j];
         if (th.at[j] < 0 || p == 0.0f) continue;
         const float logp = Vec<EB>::ld1(t + (size_t)j * EB) / a.temperature - zmax - logs;
-        const float logq = Vec<EB>::ld1(z + (size_t)th.at[j] * EB) / a.temperature - lse;
+        const float logq =
+            (Vec<EB>::ld1(z + (size_t)th.at[j] * EB) - base) / a.temperature - logz;
         s = __builtin_fmaf(p, logp - logq, s);
     }
     __syncthreads();   // th.red is free again
@@ -154,25 +155,85 @@ __device__ __forceinline__ Soft block_soft(Soft v, float c, Soft* lds) {
     return v;
 }
 
-// Column chunks of a row: chunk elements each (a multiple of a unit), `parts`
-// of them.
-template <int EB>
-__global__ __launch_bounds__(kThreads) void k_distill_part(const DistillArgs a, size_t parts,
-                                                           size_t chunk) {
+// A wavefront's maximum and sum over its lanes'.
+__device__ __forceinline__ Soft wave_soft(Soft v, float c) {
+    const float m = wave_max(v.m);
+    return {m, wave_sum(v.s * exp2_fast((soft_from(v.m) - soft_base(m)) * c))};
+}
+// G units added to a thread's share.  Values are taken from the maximum before
+// they are scaled: scaled first (one fma less), a row of the type's lowest
+// value would overflow.
+template <int EB, int G>
+__device__ __forceinline__ void soft_units(Soft& a, const u32x4* u, float c) {
     constexpr int E = Vec<EB>::E;
+    float m = a.m;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float v[E];
+        Vec<EB>::unpack(u[g], v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) m = fmaxf(m, v[j]);
+    }
+    const float base = soft_base(m);
+    float s = a.s * exp2_fast((soft_from(a.m) - base) * c);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float v[E];
+        Vec<EB>::unpack(u[g], v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) s += exp2_fast((v[j] - base) * c);
+    }
+    a.m = m;
+    a.s = s;
+}
+
+// Units of a row's chunk in registers: thread x of NT holds units
+// lo + u * NT + x for u < UPT, -inf where the chunk or the row ends.
+template <int EB, int UPT, int NT>
+struct Chunk {
+    static constexpr int E = Vec<EB>::E;
+    u32x4 raw[UPT];
+    __device__ __forceinline__ static Place place(unsigned lo, int u, unsigned vocab) {
+        return place_unit<E>((lo + u * NT + offset_here(threadIdx.x)) * E, vocab);
+    }
+    __device__ __forceinline__ void load(const char* z, unsigned lo, unsigned vocab) {
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) raw[u] = ld_unit<EB, true>(z + place(lo, u, vocab).at * EB);
+    }
+    __device__ __forceinline__ void sum(Soft& acc, unsigned lo, unsigned vocab, float c) {
+        constexpr uint32_t kNinf = EB == 2 ? 0xff80ff80u : 0xff800000u;
+        constexpr int G = UPT < 4 ? UPT : 4;
+#pragma unroll
+        for (int u = 0; u < UPT; u += G) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int skip = place(lo, u + g, vocab).skip;
+                if (skip) raw[u + g] = fill_first<EB>(raw[u + g], skip, kNinf);
+            }
+            soft_units<EB, G>(acc, raw + u, c);
+        }
+    }
+};
+
+// Maximum and sum of each chunk of each row; a row has `parts` of them.  Rows
+// shorter than a unit (SHORT) are one chunk, a value a lane.
+template <int EB, int UPT, bool SHORT>
+__global__ __launch_bounds__(kThreads) void k_distill_part(const DistillArgs a, size_t parts) {
     __shared__ Soft lds[kWaves];
     const float c = kLog2e / a.temperature;
     for (size_t task = blockIdx.x; task < a.rows * parts; task += gridDim.x) {
-        const size_t r = task / parts, lo = (task % parts) * chunk;
-        const size_t hi = lo + chunk < a.vocab ? lo + chunk : a.vocab;
+        const size_t r = task / parts;
         const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
-        const uint32_t ninf = EB == 2 ? 0xff80ff80u : 0xff800000u;
         Soft acc = soft_zero();
-        for (size_t i = lo + (size_t)threadIdx.x * E; i < hi; i += (size_t)kThreads * E) {
-            float v[E];
-            // (a tail element's bits sit in the low half of `fill`)
-            Vec<EB>::unpack(ld_unit_of<EB>(z, i, hi, ninf), v);
-            soft_add<E>(acc, v, c);
+        if constexpr (SHORT) {
+            const float one[1] = {threadIdx.x < a.vocab ? Vec<EB>::ld1(z + threadIdx.x * EB)
+                                                        : -INFINITY};
+            soft_add<1>(acc, one, c);
+        } else {
+            const unsigned lo = (unsigned)(task % parts) * (UPT * kThreads);
+            Chunk<EB, UPT, kThreads> ch;
+            ch.load(z, lo, (unsigned)a.vocab);
+            ch.sum(acc, lo, (unsigned)a.vocab, c);
         }
         acc = block_soft<kWaves>(acc, c, lds);
         if (threadIdx.x == 0) {
@@ -206,29 +267,68 @@ __global__ __launch_bounds__(kThreads) void k_distill_loss(const DistillArgs a, 
         const float lse = soft_lse(v, a.temperature);
         float zmax, logs;
         const bool some = load_teacher<EB, IB, kWaves>(a, r, th, &zmax, &logs);
-        float loss = row_loss<EB, IB, kWaves>(a, r, th, zmax, logs, lse);
+        const float loss =
+            row_loss<EB, IB, kWaves>(a, r, th, zmax, logs, soft_base(v.m), logf(v.s));
         if (threadIdx.x == 0) {
             a.loss[r] = some ? loss : 0.0f;
-            if (a.lse) a.lse[r] = lse;
+            a.lse[r] = lse;
         }
         __syncthreads();
     }
 }
 
-// The gradient of one chunk of a row.  q from the parts (PARTS) or from lse_in.
+// Loss and lse in one launch, a block per row: the next chunk's units are
+// loaded before this one's are added up.
+template <int EB, int IB>
+__global__ __launch_bounds__(kThreads) void k_distill_loss_rows(const DistillArgs a) {
+    constexpr int UPT = 4;
+    __shared__ Teacher th;
+    __shared__ Soft lds[kWaves];
+    const float c = kLog2e / a.temperature;
+    const unsigned vocab = (unsigned)a.vocab, units = (vocab + Vec<EB>::E - 1) / Vec<EB>::E;
+    for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
+        Chunk<EB, UPT, kThreads> now, next;
+        now.load(z, 0, vocab);
+        Soft acc = soft_zero();
+        for (unsigned lo = 0; lo < units; lo += UPT * kThreads) {
+            if (lo + UPT * kThreads < units) next.load(z, lo + UPT * kThreads, vocab);
+            now.sum(acc, lo, vocab, c);
+            now = next;
+        }
+        acc = block_soft<kWaves>(acc, c, lds);
+        const float lse = soft_lse(acc, a.temperature);
+        float zmax, logs;
+        const bool some = load_teacher<EB, IB, kWaves>(a, r, th, &zmax, &logs);
+        const float loss =
+            row_loss<EB, IB, kWaves>(a, r, th, zmax, logs, soft_base(acc.m), logf(acc.s));
+        if (threadIdx.x == 0) {
+            a.loss[r] = some ? loss : 0.0f;
+            a.lse[r] = lse;
+        }
+        __syncthreads();
+    }
+}
+
+// The gradient of one chunk of a row, q from the parts (PARTS) or from lse_in.
+// The chunk's loads are on their way while the teacher's entries are staged.
 // The kept entries are written after the rest of the chunk, each place by the
 // first entry that names it with the sum of its duplicates.
-template <int EB, int IB, bool PARTS>
+template <int EB, int IB, int UPT, bool PARTS>
 __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, size_t parts,
-                                                           size_t chunk, size_t soft_parts) {
+                                                           size_t soft_parts) {
     constexpr int E = Vec<EB>::E;
     __shared__ Teacher th;
-    const float c = kLog2e / a.temperature;
+    const float c = kLog2e / a.temperature, it = 1.0f / a.temperature;
+    const unsigned vocab = (unsigned)a.vocab;
     for (size_t task = blockIdx.x; task < a.rows * parts; task += gridDim.x) {
-        const size_t r = task / parts, lo = (task % parts) * chunk;
-        const size_t hi = lo + chunk < a.vocab ? lo + chunk : a.vocab;
+        const size_t r = task / parts;
+        const unsigned lo = (unsigned)(task % parts) * (UPT * kThreads);
         const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
         char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;
+        Chunk<EB, UPT, kThreads> ch;
+        const bool is_short = vocab < E;   // no 16 bytes in a row: a value a lane below
+        if (!is_short) ch.load(z, lo, vocab);
         float zmax, logs;
         const bool some = load_teacher<EB, IB, kWaves>(a, r, th, &zmax, &logs);
         const float scale = a.dloss[r] * a.temperature;
@@ -239,7 +339,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
             inv = 1.0f / v.s;
             if (lo == 0) {   // (uniform over the block)
                 const float loss =
-                    row_loss<EB, IB, kWaves>(a, r, th, zmax, logs, soft_lse(v, a.temperature));
+                    row_loss<EB, IB, kWaves>(a, r, th, zmax, logs, base, logf(v.s));
                 if (threadIdx.x == 0) a.loss[r] = some ? loss : 0.0f;
             }
         } else {
@@ -247,20 +347,33 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
         }
         const auto prob = [&](float v) -> float {
             if constexpr (PARTS) return exp2_fast((v - base) * c) * inv;
-            else return expf(v / a.temperature - lse);
+            // (fp32 results keep the digits that the scaled exponent would lose)
+            const float x = __builtin_fmaf(v, it, -lse);
+            return EB == 2 ? exp2_fast(x * kLog2e) : expf(x);
         };
-        for (size_t i = lo + (size_t)threadIdx.x * E; i < hi; i += (size_t)kThreads * E) {
-            float v[E];
-            Vec<EB>::unpack(ld_unit_of<EB>(z, i, hi, 0u), v);
+        if (!is_short) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = some ? prob(v[j]) * scale : 0.0f;
-            st_unit_of<EB>(dz, i, hi, Vec<EB>::pack(v));
+            for (int u = 0; u < UPT; ++u) {
+                u32x4 out = {0u, 0u, 0u, 0u};
+                if (some) {
+                    float v[E];
+                    Vec<EB>::unpack(ch.raw[u], v);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = prob(v[j]) * scale;
+                    out = Vec<EB>::pack(v);
+                }
+                st_place<EB, true, true>(dz, ch.place(lo, u, vocab), out);
+            }
+        } else if (threadIdx.x < vocab) {
+            const float q = some ? prob(Vec<EB>::ld1(z + threadIdx.x * EB)) * scale : 0.0f;
+            Vec<EB>::st1(dz + threadIdx.x * EB, q);
         }
         __syncthreads();
+        const unsigned from = lo * E, to = from + UPT * kThreads * E;
         if (some)
             for (int j = threadIdx.x; j < (int)a.top; j += kThreads) {
                 const int at = th.at[j];
-                if (at < 0 || (size_t)at < lo || (size_t)at >= hi) continue;
+                if (at < 0 || (unsigned)at < from || (unsigned)at >= to) continue;
                 float p = 0.0f;
                 bool mine = true;
                 for (int k = 0; k < (int)a.top; ++k)
@@ -292,38 +405,6 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
 struct RowSums {
     float m[16], s[16], tm[16], ts[16], loss[16];
 };
-// A wavefront's maximum and sum over its lanes'.
-__device__ __forceinline__ Soft wave_soft(Soft v, float c) {
-    const float m = wave_max(v.m);
-    return {m, wave_sum(v.s * exp2_fast((soft_from(v.m) - soft_base(m)) * c))};
-}
-// G units added to a thread's share.  Values are taken from the maximum before
-// they are scaled: scaled first (one fma less), a row of the type's lowest
-// value would overflow.
-template <int EB, int G>
-__device__ __forceinline__ void soft_units(Soft& a, const u32x4* u, float c) {
-    constexpr int E = Vec<EB>::E;
-    float m = a.m;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        float v[E];
-        Vec<EB>::unpack(u[g], v);
-#pragma unroll
-        for (int j = 0; j < E; ++j) m = fmaxf(m, v[j]);
-    }
-    const float base = soft_base(m);
-    float s = a.s * exp2_fast((soft_from(a.m) - base) * c);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        float v[E];
-        Vec<EB>::unpack(u[g], v);
-#pragma unroll
-        for (int j = 0; j < E; ++j) s += exp2_fast((v[j] - base) * c);
-    }
-    a.m = m;
-    a.s = s;
-}
-
 template <int EB, int IB, int UPT>
 __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     constexpr int E = Vec<EB>::E;
@@ -424,7 +505,7 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
         ts = wave_soft({has ? red[b].tm[w] : -INFINITY, has ? red[b].ts[w] : 0.0f}, c);
         const bool some = !(ts.s == 0.0f);
         const float scale = a.dloss[r] * a.temperature;
-        const float base = soft_base(zs.m), lse = soft_lse(zs, a.temperature);
+        const float base = soft_base(zs.m), logz = logf(zs.s);
         const float tbase = soft_base(ts.m), logs = logf(ts.s), tinv = 1.0f / ts.s;
         char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;
 
@@ -433,7 +514,8 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
         const auto term = [&](int j, float zj) {
             const float p = prob(j);
             if (at[b][j] < 0 || p == 0.0f) return 0.0f;
-            return p * ((tz[b][j] - tbase) / a.temperature - logs - (zj / a.temperature - lse));
+            return p * ((tz[b][j] - tbase) / a.temperature - logs -
+                        ((zj - base) / a.temperature - logz));
         };
         const auto patch = [&](int j, float zj, float* v) {
             const int mine = at[b][j];
@@ -512,18 +594,17 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     if (r >= gridDim.x) settle_row(r - gridDim.x, b ^ 1);
 }
 
-// The split of a row into chunks: kChunkBytes, more blocks for few rows.
+// The split of rows into chunks of UPT units a thread: 8, or 2 where there are
+// too few chunks of 8 for the card's compute units.
 struct Split {
-    size_t parts, chunk;
+    int upt;
+    size_t parts;
 };
 Split split_of(size_t rows, size_t vocab, int eb) {
-    const size_t e = 16 / eb, unit = (size_t)kThreads * e;   // one unit per thread
-    size_t parts = (vocab + 16 * unit - 1) / (16 * unit);
-    const size_t most = (vocab + unit - 1) / unit;
-    while (rows * parts < 512 && parts < most) parts = parts * 2 < most ? parts * 2 : most;
-    size_t chunk = (vocab + parts - 1) / parts;
-    chunk = (chunk + e - 1) / e * e;
-    return {(vocab + chunk - 1) / chunk, chunk};
+    const size_t e = 16 / (size_t)eb, units = (vocab + e - 1) / e;
+    const size_t parts = (units + 8 * kThreads - 1) / (8 * kThreads);
+    if (rows * parts >= 1024) return {8, parts};
+    return {2, (units + 2 * kThreads - 1) / (2 * kThreads)};
 }
 
 // The register form of a step: units per thread and threads; upt 0: the row
@@ -561,24 +642,63 @@ unsigned grid_of(size_t tasks) {
 
 hipError_t launch_part(const DistillArgs& a, Split sp, hipStream_t s) {
     const dim3 grid(grid_of(a.rows * sp.parts)), block(kThreads);
-    if (a.eb == 2) hipLaunchKernelGGL(k_distill_part<2>, grid, block, 0, s, a, sp.parts, sp.chunk);
-    else hipLaunchKernelGGL(k_distill_part<4>, grid, block, 0, s, a, sp.parts, sp.chunk);
+#define CALL(EB, UPT, SHORT) \
+    hipLaunchKernelGGL((k_distill_part<EB, UPT, SHORT>), grid, block, 0, s, a, sp.parts)
+    if (a.vocab < (size_t)(16 / a.eb)) {
+        if (a.eb == 2) CALL(2, 2, true);
+        else CALL(4, 2, true);
+    } else if (sp.upt == 8) {
+        if (a.eb == 2) CALL(2, 8, false);
+        else CALL(4, 8, false);
+    } else {
+        if (a.eb == 2) CALL(2, 2, false);
+        else CALL(4, 2, false);
+    }
+#undef CALL
     return hipGetLastError();
+}
+
+template <bool PARTS>
+hipError_t launch_grad(const DistillArgs& a, Split sp, hipStream_t s) {
+    const dim3 grid(grid_of(a.rows * sp.parts)), block(kThreads);
+#define CALL(EB, IB)                                                                              \
+    if (sp.upt == 8)                                                                              \
+        hipLaunchKernelGGL((k_distill_grad<EB, IB, 8, PARTS>), grid, block, 0, s, a, sp.parts,    \
+                           sp.parts);                                                             \
+    else                                                                                          \
+        hipLaunchKernelGGL((k_distill_grad<EB, IB, 2, PARTS>), grid, block, 0, s, a, sp.parts,    \
+                           sp.parts)
+    DISTILL_BY_TYPE(CALL);
+#undef CALL
+    return hipGetLastError();
+}
+
+// From this many rows on the loss takes a block per row and one launch.
+constexpr size_t kLossRows = 512;
+bool loss_by_rows(size_t rows, size_t vocab, int eb) {
+    return rows >= kLossRows && vocab >= (size_t)(16 / eb);
 }
 
 }  // namespace
 
 size_t distill_work_floats(size_t rows, size_t vocab, int eb, bool step) {
-    if (rows == 0 || (step && row_fit(rows, vocab, eb).upt)) return 0;
+    if (rows == 0 || (step ? row_fit(rows, vocab, eb).upt != 0 : loss_by_rows(rows, vocab, eb)))
+        return 0;
     return 2 * rows * split_of(rows, vocab, eb).parts;
 }
 
 hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
+    const dim3 grid(grid_of(a.rows)), block(kThreads);
+    if (loss_by_rows(a.rows, a.vocab, a.eb)) {
+#define CALL(EB, IB) hipLaunchKernelGGL((k_distill_loss_rows<EB, IB>), grid, block, 0, s, a)
+        DISTILL_BY_TYPE(CALL);
+#undef CALL
+        return hipGetLastError();
+    }
     const Split sp = split_of(a.rows, a.vocab, a.eb);
     const hipError_t e = launch_part(a, sp, s);
     if (e != hipSuccess) return e;
-    const dim3 grid(grid_of(a.rows)), block(kThreads);
 #define CALL(EB, IB) hipLaunchKernelGGL((k_distill_loss<EB, IB>), grid, block, 0, s, a, sp.parts)
     DISTILL_BY_TYPE(CALL);
 #undef CALL
@@ -587,14 +707,7 @@ hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s) {
 
 hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    const Split sp = split_of(a.rows, a.vocab, a.eb);
-    const dim3 grid(grid_of(a.rows * sp.parts)), block(kThreads);
-#define CALL(EB, IB) \
-    hipLaunchKernelGGL((k_distill_grad<EB, IB, false>), grid, block, 0, s, a, sp.parts, sp.chunk, \
-                       size_t(0))
-    DISTILL_BY_TYPE(CALL);
-#undef CALL
-    return hipGetLastError();
+    return launch_grad<false>(a, split_of(a.rows, a.vocab, a.eb), s);
 }
 
 hipError_t launch_distill_step(const DistillArgs& a, hipStream_t s) {
@@ -614,14 +727,7 @@ hipError_t launch_distill_step(const DistillArgs& a, hipStream_t s) {
     }
     const Split sp = split_of(a.rows, a.vocab, a.eb);
     const hipError_t e = launch_part(a, sp, s);
-    if (e != hipSuccess) return e;
-    const dim3 grid(grid_of(a.rows * sp.parts)), block(kThreads);
-#define CALL(EB, IB) \
-    hipLaunchKernelGGL((k_distill_grad<EB, IB, true>), grid, block, 0, s, a, sp.parts, sp.chunk, \
-                       sp.parts)
-    DISTILL_BY_TYPE(CALL);
-#undef CALL
-    return hipGetLastError();
+    return e != hipSuccess ? e : launch_grad<true>(a, sp, s);
 }
 
 }  // namespace arlib

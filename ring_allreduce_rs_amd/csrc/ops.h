@@ -91,7 +91,7 @@ struct DistillArgs {
     const float* dloss;   // gradient passes
     const float* lse_in;  // backward: the forward pass's lse
     float* loss;
-    float* lse;           // NULL: not wanted
+    float* lse;
     void* dlogits;
     float* part;          // distill_work_floats() floats
     size_t lstride;

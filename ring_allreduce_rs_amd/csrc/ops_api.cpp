@@ -23,7 +23,7 @@ size_t float_bytes(int dtype) {
     return dtype == AR_BFLOAT16 ? 2 : dtype == AR_FLOAT32 ? 4 : 0;
 }
 
-// Widest row of a layer norm and of the experts (byte offsets within a row stay
+// Widest row of a layer norm, of the experts and of the logits (byte offsets within a row stay
 // below 2^32, and so do the column sums' threads).
 constexpr size_t kMostCols = size_t(1) << 28;
 
@@ -165,8 +165,8 @@ ar_status check_distill(ar_ctx* ctx, Arrays& arrays, arlib::DistillArgs& d, cons
     const ar_status s = check_index_bytes(ctx, index_bytes);
     if (s != AR_OK) return s;
     if (vocab < 1 || top < 1) return fail(ctx, AR_ERR_INVALID_ARG, "vocab or top is 0");
-    if (vocab > (size_t)INT_MAX)
-        return fail(ctx, AR_ERR_UNSUPPORTED, "vocab %zu above 2^31 - 1", vocab);
+    if (vocab > kMostCols)
+        return fail(ctx, AR_ERR_UNSUPPORTED, "vocab %zu above 2^28", vocab);
     if (top > AR_DISTILL_MAX_TOP)
         return fail(ctx, AR_ERR_UNSUPPORTED, "top %zu above %d", top, AR_DISTILL_MAX_TOP);
     if (!(temperature > 0.0f) || std::isinf(temperature))

@@ -137,6 +137,26 @@ def test_non_finite_rows_stay_alone(vocab, t):
     assert torch.equal(b[good], clean_b[good]) and torch.isnan(b[1]).all()
 
 
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("rows,vocab", [(3, 5), (3, 700), (2, 32000), (600, 4099), (2, 140001)])
+def test_rows_of_the_lowest_value(rows, vocab, t):
+    """Every logit of a row masked by the type's lowest value: all are equal, so
+    both softmaxes are uniform."""
+    logits, at, teacher, dloss = make(rows, vocab, 4, t, 3, pad=0.0)
+    at = torch.arange(4, device="cuda").expand(rows, 4).contiguous()
+    logits[1] = torch.finfo(t).min
+    teacher[1] = torch.finfo(t).min
+    check(logits, at, teacher, dloss, 1.0)
+    loss, d = ar.distill_step(dloss, logits, at, teacher, 2.0)
+    # log(vocab / 4): four logarithms and exponentials of 0, the sum's additions
+    bound = (ref.depth(vocab) + 16) * 4 * ref.U * (1 + math.log(vocab))
+    assert abs(float(loss[1]) - 4 * math.log(vocab / 4)) <= 4 * bound
+    q = torch.full((vocab,), 1 / vocab, dtype=torch.float64, device="cuda")
+    q[:4] -= 0.25
+    want = q * dloss[1].double() * 2
+    ref.close(d[1], want, want.abs() * (bound + ref.half_step(t)) + bound / vocab * want.abs().max())
+
+
 def test_a_row_of_minus_infinity():
     logits, at, teacher, dloss = make(3, 5000, 8, F32, 9, pad=0.0)
     logits[1] = -math.inf
