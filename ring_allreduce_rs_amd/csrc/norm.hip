@@ -9,6 +9,8 @@
 // All sums and statistics are fp32; each output is rounded once.  The variance
 // is taken from the centred values (a second pass over the row), so a mean far
 // larger than the spread costs no digits.
+#include <cmath>
+
 #include "ops.h"
 #include "ops_device.h"
 
@@ -21,6 +23,187 @@ constexpr int kNormWaves = kNormThreads / 64;
 __device__ __forceinline__ void st_param(void* base, int pb, size_t i, float v) {
     if (pb == 4) Vec<4>::st1(static_cast<char*>(base) + i * 4, v);
     else Vec<2>::st1(static_cast<char*>(base) + i * 2, v);
+}
+
+// Narrow rows: TPR lanes a row (a power of two below 64), so that a wavefront
+// takes 64 / TPR rows at once, and kNarrowSteps such steps in flight.
+constexpr int kNarrowSteps = 4;
+
+// Sum over the TPR lanes of a row, on each of them.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v) {
+    static_assert(TPR == 8 || TPR == 16 || TPR == 32, "lanes of a row");
+    v += dpp<kDppSwap1, 0xf>(0.0f, v);
+    v += dpp<kDppSwap2, 0xf>(0.0f, v);
+    v += dpp<kDppHalfMirror, 0xf>(0.0f, v);
+    if constexpr (TPR > 8) v += dpp<kDppMirror, 0xf>(0.0f, v);
+    if constexpr (TPR > 16) v += __shfl_xor(v, 16, 64);
+    return v;
+}
+
+template <int EB, int TPR, bool RAGGED>
+__global__ __launch_bounds__(kNormThreads) void k_norm_narrow(const NormArgs a) {
+    constexpr int E = Vec<EB>::E, RW = 64 / TPR, RB = kNormWaves * kNarrowSteps * RW;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const float n = (float)a.cols;
+    const Place at = place_unit<E>((lane % TPR) * E, (unsigned)a.cols);
+    float w[E], b[E];
+    ld_params<E>(a.weight, a.pb, at.at, a.cols, 1.0f, w);
+    ld_params<E>(a.bias, a.pb, at.at, a.cols, 0.0f, b);
+    for (size_t r0 = (size_t)blockIdx.x * RB; r0 < a.rows; r0 += (size_t)gridDim.x * RB) {
+        u32x4 raw[kNarrowSteps];
+        const size_t first = r0 + (size_t)wave * (kNarrowSteps * RW) + lane / TPR;
+#pragma unroll
+        for (int k = 0; k < kNarrowSteps; ++k) {
+            const size_t r = first + k * RW < a.rows ? first + k * RW : a.rows - 1;
+            raw[k] = ld_unit<EB>(static_cast<const char*>(a.x) + (r * a.xstride + at.at) * EB);
+        }
+#pragma unroll
+        for (int k = 0; k < kNarrowSteps; ++k) {
+            const size_t r = first + k * RW;
+            if (at.skip) raw[k] = drop_first<EB, RAGGED>(raw[k], at.skip);
+            float v[E], s = 0.0f;
+            Vec<EB>::unpack(raw[k], v);
+#pragma unroll
+            for (int j = 0; j < E; ++j) s += v[j];
+            const float mean = row_sum<TPR>(s) / n;
+            s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const float d = (RAGGED ? j < at.skip : at.skip != 0) ? 0.0f : v[j] - mean;
+                s = __builtin_fmaf(d, d, s);
+            }
+            const float rstd = 1.0f / sqrtf(row_sum<TPR>(s) / n + a.eps);
+            if (r >= a.rows) continue;
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[j], b[j]);
+            st_place<EB, RAGGED, true>(static_cast<char*>(a.y) + r * a.cols * EB, at,
+                                       Vec<EB>::pack(v));
+            if (lane % TPR == 0) {
+                a.mean[r] = mean;
+                a.rstd[r] = rstd;
+            }
+        }
+    }
+}
+
+// E values at columns c ... of an array of `pb`-byte elements, the first `skip`
+// left out.
+template <int E>
+__device__ __forceinline__ void st_params(void* base, int pb, size_t c, int skip,
+                                          const float (&v)[E]) {
+    char* p = static_cast<char*>(base) + c * pb;
+    if (skip == 0 && pb == 4) {
+#pragma unroll
+        for (int h = 0; h < E / 4; ++h)
+            st_unit<4>(p + 16 * h, u32x4{as_u32(v[4 * h]), as_u32(v[4 * h + 1]),
+                                         as_u32(v[4 * h + 2]), as_u32(v[4 * h + 3])});
+        return;
+    }
+    if constexpr (E == 8)
+        if (skip == 0) {
+            st_unit<2>(p, Vec<2>::pack(v));
+            return;
+        }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (j >= skip) st_param(base, pb, c + j, v[j]);
+}
+
+// Column sums' last stop: a row of partial sums, or the gradients themselves
+// where there is no other part.
+template <int E>
+__device__ __forceinline__ void put_columns(const NormGradArgs& a, Place at, const float (&dw)[E],
+                                            const float (&db)[E]) {
+    if (at.skip >= E) return;
+    if (gridDim.x > 1) {
+        float* out = a.part + (size_t)blockIdx.x * 2 * a.cols;
+        st_params<E>(out, 4, at.at, at.skip, dw);
+        st_params<E>(out + a.cols, 4, at.at, at.skip, db);
+    } else {
+        if (a.dweight) st_params<E>(a.dweight, a.pb, at.at, at.skip, dw);
+        if (a.dbias) st_params<E>(a.dbias, a.pb, at.at, at.skip, db);
+    }
+}
+
+template <int EB, int TPR, bool RAGGED>
+__global__ __launch_bounds__(kNormThreads) void k_norm_grad_narrow(const NormGradArgs a) {
+    constexpr int E = Vec<EB>::E, RW = 64 / TPR, RB = kNormWaves * kNarrowSteps * RW;
+    __shared__ float lds[kNormWaves][2 * E][TPR];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const float inv = 1.0f / (float)a.cols;
+    const Place at = place_unit<E>((lane % TPR) * E, (unsigned)a.cols);
+    float w[E], dw[E], db[E];
+    ld_params<E>(a.weight, a.pb, at.at, a.cols, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < E; ++j) dw[j] = db[j] = 0.0f;
+    for (size_t r0 = (size_t)blockIdx.x * RB; r0 < a.rows; r0 += (size_t)gridDim.x * RB) {
+        u32x4 rx[kNarrowSteps], rg[kNarrowSteps];
+        float mean[kNarrowSteps], rstd[kNarrowSteps];
+        const size_t first = r0 + (size_t)wave * (kNarrowSteps * RW) + lane / TPR;
+#pragma unroll
+        for (int k = 0; k < kNarrowSteps; ++k) {
+            const size_t r = first + k * RW < a.rows ? first + k * RW : a.rows - 1;
+            rx[k] = ld_unit<EB>(static_cast<const char*>(a.x) + (r * a.xstride + at.at) * EB);
+            rg[k] = ld_unit<EB>(static_cast<const char*>(a.dy) + (r * a.dystride + at.at) * EB);
+            mean[k] = a.mean[r];
+            rstd[k] = a.rstd[r];
+        }
+#pragma unroll
+        for (int k = 0; k < kNarrowSteps; ++k) {
+            const size_t r = first + k * RW;
+            const int skip = r < a.rows ? at.skip : E;
+            if (skip) {
+                rx[k] = drop_first<EB, RAGGED>(rx[k], skip);
+                rg[k] = drop_first<EB, RAGGED>(rg[k], skip);
+            }
+            float v[E], g[E], s1 = 0.0f, s2 = 0.0f;
+            Vec<EB>::unpack(rx[k], v);
+            Vec<EB>::unpack(rg[k], g);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                v[j] = (v[j] - mean[k]) * rstd[k];
+                db[j] += g[j];
+                // (past the last row nothing counts, whatever that row holds)
+                dw[j] = skip == E ? dw[j] : __builtin_fmaf(g[j], v[j], dw[j]);
+                g[j] *= w[j];
+                s1 += g[j];
+                s2 = __builtin_fmaf(g[j], v[j], s2);
+            }
+            const float c1 = row_sum<TPR>(s1) * inv, c2 = row_sum<TPR>(s2) * inv;
+            if (r >= a.rows) continue;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                v[j] = rstd[k] * __builtin_fmaf(-v[j], c2, g[j] - c1);
+            st_place<EB, RAGGED>(static_cast<char*>(a.dx) + r * a.cols * EB, at, Vec<EB>::pack(v));
+        }
+    }
+    if (!a.dweight && !a.dbias) return;
+    // the wavefront's rows, then the wavefronts
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+#pragma unroll
+        for (int d = TPR; d < 64; d <<= 1) {
+            dw[j] += __shfl_xor(dw[j], d, 64);
+            db[j] += __shfl_xor(db[j], d, 64);
+        }
+        if (lane < TPR) {
+            lds[wave][j][lane] = dw[j];
+            lds[wave][E + j][lane] = db[j];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x >= TPR) return;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        dw[j] = db[j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kNormWaves; ++k) {
+            dw[j] += lds[k][j][lane];
+            db[j] += lds[k][E + j][lane];
+        }
+    }
+    put_columns<E>(a, at, dw, db);
 }
 
 // Rows that a block holds in registers: NT threads with UPT units each, R rows
@@ -202,21 +385,8 @@ __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
         }
     }
     if (!a.dweight && !a.dbias) return;
-    float* out = a.part + (size_t)blockIdx.x * 2 * a.cols;
 #pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (RAGGED ? j >= at[u].skip : at[u].skip == 0) {
-                const size_t c = at[u].at + j;
-                if (gridDim.x > 1) {
-                    out[c] = dw[u][j];
-                    out[a.cols + c] = db[u][j];
-                } else {   // no other part: these are the sums
-                    if (a.dweight) st_param(a.dweight, a.pb, c, dw[u][j]);
-                    if (a.dbias) st_param(a.dbias, a.pb, c, db[u][j]);
-                }
-            }
+    for (int u = 0; u < UPT; ++u) put_columns<E>(a, at[u], dw[u], db[u]);
 }
 
 // Rows of any width: one block per row, three walks over it (the second and
@@ -354,7 +524,7 @@ __global__ __launch_bounds__(kFoldThreads) void k_norm_fold(const NormGradArgs a
     float s = 0.0f;
     if (c < 2 * a.cols) {
         const float* p = a.part + c;
-#pragma unroll 8
+#pragma unroll 16
         for (size_t k = wave; k < parts; k += kFoldWaves) s += p[k * 2 * a.cols];
     }
     lds[wave][lane] = s;
@@ -376,35 +546,46 @@ static unsigned row_blocks(size_t rows) {
 
 // The shape of a row kernel: threads, units per thread and rows at a time;
 // threads 0: rows too wide for registers, or narrower than a unit, are the wide
-// kernels'.
+// kernels'; threads below 64: the narrow kernels', that many lanes a row.
 struct RowShape {
     int threads, upt, r;
 };
 static RowShape row_shape(size_t cols, int eb) {
     if (cols < 16u / eb) return {0, 0, 0};   // no 16 bytes in a row
     const size_t units = (cols * eb + 15) / 16;
+    if (units <= 32) {
+        const int tpr = units <= 8 ? 8 : units <= 16 ? 16 : 32;
+        return {tpr, 1, kNormWaves * kNarrowSteps * 64 / tpr};
+    }
     if (units <= 64) return {64, 1, 4};
     if (units <= 256) return {256, 1, 4};
     if (units <= 512) return {512, 1, 4};
     if (units <= 1024) return {1024, 1, 4};
-    if (units <= 2048) return {1024, 2, 2};
+    if (units <= 2048) return {1024, 2, 1};
     if (units <= 4096 && eb == 4) return {1024, 4, 1};
     return {0, 0, 0};
 }
 
-// Blocks of the backward row kernel: enough wavefronts for every compute unit
-// (16 each), but at least kRowsPerPart rows for each row of partial sums that a
-// block leaves.
-constexpr size_t kRowsPerPart = 16;
-static size_t grad_blocks(size_t rows, RowShape sh) {
-    if (rows <= kRowsPerPart) return rows ? 1 : 0;
-    const size_t most = 4096 / (sh.threads / 64), want = (rows + kRowsPerPart - 1) / kRowsPerPart;
-    return want < most ? want : most;
+// Blocks of the backward row kernels, each of which leaves a row of partial
+// sums.  More blocks share out the steps over the rows (about 3 us a step of R
+// rows, mostly latency), and cost the last step more: 8 bytes a column and
+// block at about 4 TB/s, or about 1/160 us a block where there are few columns
+// and the additions follow one another.  With both costs c, P blocks of S steps
+// in all take 3 S / P + c P, the least at P = sqrt(3 S / c).  Two steps of one
+// block are cheaper than a second launch.
+static size_t grad_blocks(size_t rows, size_t cols, RowShape sh) {
+    const size_t steps = (rows + sh.r - 1) / sh.r;
+    if (steps <= 2) return rows ? 1 : 0;
+    const size_t most = sh.threads < 64 ? 1024 : 4096 / (sh.threads / 64);
+    const double c = cols * 2e-6 > 0.00625 ? cols * 2e-6 : 0.00625;
+    const size_t best = (size_t)std::sqrt(3.0 * (double)steps / c) + 1;
+    const size_t p = best < most ? best : most;
+    return p < steps ? p : steps;
 }
 
 size_t norm_grad_parts(size_t rows, size_t cols, int eb) {
     const RowShape sh = row_shape(cols, eb);
-    if (sh.threads) return grad_blocks(rows, sh);
+    if (sh.threads) return grad_blocks(rows, cols, sh);
     const size_t p = (rows + kColRows - 1) / kColRows;
     return p < kColParts ? p : kColParts;
 }
@@ -415,16 +596,20 @@ size_t norm_grad_parts(size_t rows, size_t cols, int eb) {
         case 256 * 8 + 1: CALL(EB, 256, 1, 4, RAGGED); break;                 \
         case 512 * 8 + 1: CALL(EB, 512, 1, 4, RAGGED); break;                 \
         case 1024 * 8 + 1: CALL(EB, 1024, 1, 4, RAGGED); break;               \
-        case 1024 * 8 + 2: CALL(EB, 1024, 2, 2, RAGGED); break;               \
+        case 1024 * 8 + 2: CALL(EB, 1024, 2, 1, RAGGED); break;               \
         default: if constexpr (EB == 4) CALL(EB, 1024, 4, 1, RAGGED); break;  \
     }
+#define NARROW_BY_SHAPE(EB, RAGGED, CALL)                   \
+    if (sh.threads == 8) { CALL(EB, 8, RAGGED); }           \
+    else if (sh.threads == 16) { CALL(EB, 16, RAGGED); }    \
+    else { CALL(EB, 32, RAGGED); }
 // RAGGED: the row's end lies inside a unit (the other form spends no
 // registers on that)
-#define ROWS_BY_TYPE(CALL)                                      \
-    if (a.cols % (16 / a.eb) == 0) {                            \
-        if (a.eb == 2) { ROWS_BY_SHAPE(2, false, CALL) } else { ROWS_BY_SHAPE(4, false, CALL) } \
-    } else {                                                    \
-        if (a.eb == 2) { ROWS_BY_SHAPE(2, true, CALL) } else { ROWS_BY_SHAPE(4, true, CALL) } \
+#define BY_TYPE(SHAPE, CALL)                                                            \
+    if (a.cols % (16 / a.eb) == 0) {                                                    \
+        if (a.eb == 2) { SHAPE(2, false, CALL) } else { SHAPE(4, false, CALL) }         \
+    } else {                                                                            \
+        if (a.eb == 2) { SHAPE(2, true, CALL) } else { SHAPE(4, true, CALL) }           \
     }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
@@ -436,10 +621,17 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
         else hipLaunchKernelGGL(k_norm_wide<4>, grid, block, 0, s, a);
         return hipGetLastError();
     }
-    const dim3 grid(row_blocks((a.rows + sh.r - 1) / sh.r)), block(sh.threads);
+    const dim3 grid(row_blocks((a.rows + sh.r - 1) / sh.r));
+    if (sh.threads < 64) {
+#define CALL(EB, TPR, RAGGED) \
+    hipLaunchKernelGGL((k_norm_narrow<EB, TPR, RAGGED>), grid, dim3(kNormThreads), 0, s, a)
+        BY_TYPE(NARROW_BY_SHAPE, CALL)
+#undef CALL
+        return hipGetLastError();
+    }
 #define CALL(EB, NT, UPT, R, RAGGED) \
-    hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, R, RAGGED>), grid, block, 0, s, a)
-    ROWS_BY_TYPE(CALL)
+    hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, R, RAGGED>), grid, dim3(NT), 0, s, a)
+    BY_TYPE(ROWS_BY_SHAPE, CALL)
 #undef CALL
     return hipGetLastError();
 }
@@ -462,11 +654,18 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
     const size_t parts = norm_grad_parts(a.rows, a.cols, a.eb);
     const RowShape sh = row_shape(a.cols, a.eb);
     if (a.rows > 0 && sh.threads) {
-        const dim3 grid((unsigned)parts), block(sh.threads);
-#define CALL(EB, NT, UPT, R, RAGGED) \
-    hipLaunchKernelGGL((k_norm_grad_rows<EB, NT, UPT, R, RAGGED>), grid, block, 0, s, a)
-        ROWS_BY_TYPE(CALL)
+        const dim3 grid((unsigned)parts);
+        if (sh.threads < 64) {
+#define CALL(EB, TPR, RAGGED) \
+    hipLaunchKernelGGL((k_norm_grad_narrow<EB, TPR, RAGGED>), grid, dim3(kNormThreads), 0, s, a)
+            BY_TYPE(NARROW_BY_SHAPE, CALL)
 #undef CALL
+        } else {
+#define CALL(EB, NT, UPT, R, RAGGED) \
+    hipLaunchKernelGGL((k_norm_grad_rows<EB, NT, UPT, R, RAGGED>), grid, dim3(NT), 0, s, a)
+            BY_TYPE(ROWS_BY_SHAPE, CALL)
+#undef CALL
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || parts == 1) return e;
     } else if (a.rows > 0) {
