@@ -17,6 +17,7 @@
 namespace arlib {
 namespace {
 
+constexpr int kCUs = 256;
 constexpr int kNormThreads = 256;
 constexpr int kNormWaves = kNormThreads / 64;
 
@@ -216,15 +217,8 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
     __shared__ float lds[2][W * R];
     const float n = (float)a.cols;
     Place at[UPT];
-    float w[UPT][E], b[UPT][E];
-#pragma unroll
-    for (int u = 0; u < UPT; ++u) {
-        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
-        ld_params<E>(a.weight, a.pb, at[u].at, a.cols, 1.0f, w[u]);
-        ld_params<E>(a.bias, a.pb, at[u].at, a.cols, 0.0f, b[u]);
-    }
-    for (size_t r0 = (size_t)blockIdx.x * R; r0 < a.rows; r0 += (size_t)gridDim.x * R) {
-        u32x4 raw[R][UPT];
+    u32x4 raw[R][UPT];
+    const auto load = [&](size_t r0) {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const size_t r = r0 + k < a.rows ? r0 + k : a.rows - 1;
@@ -233,6 +227,20 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
             for (int u = 0; u < UPT; ++u)
                 raw[k][u] = ld_unit<EB>(x + offset_here(at[u].at * EB));
         }
+    };
+#pragma unroll
+    for (int u = 0; u < UPT; ++u)
+        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
+    size_t r0 = (size_t)blockIdx.x * R;
+    load(r0);   // (ahead of the parameters: one round trip for both)
+    float w[UPT][E], b[UPT][E];
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+        ld_params<E>(a.weight, a.pb, at[u].at, a.cols, 1.0f, w[u]);
+        ld_params<E>(a.bias, a.pb, at[u].at, a.cols, 0.0f, b[u]);
+    }
+    for (; r0 < a.rows; r0 += (size_t)gridDim.x * R) {
+        if (r0 != (size_t)blockIdx.x * R) load(r0);
         float mean[R], s[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -300,32 +308,38 @@ __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
     __shared__ float lds[2][W * 2 * R];
     const float inv = 1.0f / (float)a.cols;
     Place at[UPT];
+    u32x4 rx[R][UPT], rg[R][UPT];
+    float mean[R], rstd[R];
+    const auto load = [&](size_t r0, int k) {
+        const size_t r = r0 + k < a.rows ? r0 + k : a.rows - 1;
+        const char* x = static_cast<const char*>(a.x) + r * a.xstride * EB;
+        const char* dy = static_cast<const char*>(a.dy) + r * a.dystride * EB;
+        mean[k] = ld_uniform(a.mean + r);
+        rstd[k] = ld_uniform(a.rstd + r);
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) {
+            const unsigned off = offset_here(at[u].at * EB);
+            rx[k][u] = ld_unit<EB, true>(x + off);
+            rg[k][u] = ld_unit<EB, true>(dy + off);
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < UPT; ++u)
+        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
+    size_t r0 = (size_t)blockIdx.x * R;
+#pragma unroll
+    for (int k = 0; k < R; ++k) load(r0, k);
     float w[UPT][E], dw[UPT][E], db[UPT][E];
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
         ld_params<E>(a.weight, a.pb, at[u].at, a.cols, 1.0f, w[u]);
 #pragma unroll
         for (int j = 0; j < E; ++j) dw[u][j] = db[u][j] = 0.0f;
     }
     int buf = 0;
-    for (size_t r0 = (size_t)blockIdx.x * R; r0 < a.rows; r0 += (size_t)gridDim.x * R, buf ^= 1) {
-        u32x4 rx[R][UPT], rg[R][UPT];
-        float mean[R], rstd[R], s[2 * R];
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const size_t r = r0 + k < a.rows ? r0 + k : a.rows - 1;
-            const char* x = static_cast<const char*>(a.x) + r * a.xstride * EB;
-            const char* dy = static_cast<const char*>(a.dy) + r * a.dystride * EB;
-            mean[k] = ld_uniform(a.mean + r);
-            rstd[k] = ld_uniform(a.rstd + r);
-#pragma unroll
-            for (int u = 0; u < UPT; ++u) {
-                const unsigned off = offset_here(at[u].at * EB);
-                rx[k][u] = ld_unit<EB, true>(x + off);
-                rg[k][u] = ld_unit<EB, true>(dy + off);
-            }
-        }
+    for (; r0 < a.rows; r0 += (size_t)gridDim.x * R, buf ^= 1) {
+        float s[2 * R];
+        const size_t next = r0 + (size_t)gridDim.x * R;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             float s1 = 0.0f, s2 = 0.0f;
@@ -364,7 +378,6 @@ __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
         block_sums<W, 2 * R>(s, lds[buf]);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (r0 + k >= a.rows) break;
             const float c1 = s[2 * k] * inv, c2 = s[2 * k + 1] * inv;
             char* dx = static_cast<char*>(a.dx) + (r0 + k) * a.cols * EB;
 #pragma unroll
@@ -379,8 +392,11 @@ __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
                     const float xh = (v[j] - mean[k]) * rstd[k];
                     v[j] = rstd[k] * __builtin_fmaf(-xh, c2, __builtin_fmaf(g[j], w[u][j], -c1));
                 }
-                st_place<EB, RAGGED>(dx, at[u], Vec<EB>::pack(v));
+                if (r0 + k < a.rows) st_place<EB, RAGGED>(dx, at[u], Vec<EB>::pack(v));
             }
+            // the row's registers are free: the next step's row comes in while
+            // this step goes on
+            if (next < a.rows) load(next, k);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -523,9 +539,16 @@ __global__ __launch_bounds__(kFoldThreads) void k_norm_fold(const NormGradArgs a
     const size_t c = (size_t)blockIdx.x * 64 + lane;   // of 2 * cols
     float s = 0.0f;
     if (c < 2 * a.cols) {
+        constexpr int kAhead = 16;   // loads in flight
         const float* p = a.part + c;
-#pragma unroll 16
-        for (size_t k = wave; k < parts; k += kFoldWaves) s += p[k * 2 * a.cols];
+        for (size_t k = wave; k < parts; k += kFoldWaves * kAhead) {
+            float v[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q)
+                v[q] = k + q * kFoldWaves < parts ? p[(k + q * kFoldWaves) * 2 * a.cols] : 0.0f;
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) s += v[q];
+        }
     }
     lds[wave][lane] = s;
     __syncthreads();
@@ -592,12 +615,12 @@ size_t norm_grad_parts(size_t rows, size_t cols, int eb) {
 
 #define ROWS_BY_SHAPE(EB, RAGGED, CALL)                                       \
     switch (sh.threads * 8 + sh.upt) {                                        \
-        case 64 * 8 + 1: CALL(EB, 64, 1, 4, RAGGED); break;                   \
-        case 256 * 8 + 1: CALL(EB, 256, 1, 4, RAGGED); break;                 \
-        case 512 * 8 + 1: CALL(EB, 512, 1, 4, RAGGED); break;                 \
-        case 1024 * 8 + 1: CALL(EB, 1024, 1, 4, RAGGED); break;               \
-        case 1024 * 8 + 2: CALL(EB, 1024, 2, 1, RAGGED); break;               \
-        default: if constexpr (EB == 4) CALL(EB, 1024, 4, 1, RAGGED); break;  \
+        case 64 * 8 + 1: { CALL(EB, 64, 1, 4, RAGGED); } break; \
+        case 256 * 8 + 1: { CALL(EB, 256, 1, 4, RAGGED); } break; \
+        case 512 * 8 + 1: { CALL(EB, 512, 1, 4, RAGGED); } break; \
+        case 1024 * 8 + 1: { CALL(EB, 1024, 1, 4, RAGGED); } break; \
+        case 1024 * 8 + 2: { CALL(EB, 1024, 2, 1, RAGGED); } break; \
+        default: if constexpr (EB == 4) { CALL(EB, 1024, 4, 1, RAGGED); } break; \
     }
 #define NARROW_BY_SHAPE(EB, RAGGED, CALL)                   \
     if (sh.threads == 8) { CALL(EB, 8, RAGGED); }           \
@@ -621,7 +644,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
         else hipLaunchKernelGGL(k_norm_wide<4>, grid, block, 0, s, a);
         return hipGetLastError();
     }
-    const dim3 grid(row_blocks((a.rows + sh.r - 1) / sh.r));
+    dim3 grid(row_blocks((a.rows + sh.r - 1) / sh.r));
     if (sh.threads < 64) {
 #define CALL(EB, TPR, RAGGED) \
     hipLaunchKernelGGL((k_norm_narrow<EB, TPR, RAGGED>), grid, dim3(kNormThreads), 0, s, a)
@@ -629,8 +652,12 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 #undef CALL
         return hipGetLastError();
     }
-#define CALL(EB, NT, UPT, R, RAGGED) \
-    hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, R, RAGGED>), grid, dim3(NT), 0, s, a)
+    // one row a block until every compute unit has rows at R a block
+    const bool few = a.rows <= (size_t)kCUs * sh.r;
+    if (few) grid.x = (unsigned)a.rows;
+#define CALL(EB, NT, UPT, R, RAGGED)                                                             \
+    if (few) hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, 1, RAGGED>), grid, dim3(NT), 0, s, a); \
+    else hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, R, RAGGED>), grid, dim3(NT), 0, s, a)
     BY_TYPE(ROWS_BY_SHAPE, CALL)
 #undef CALL
     return hipGetLastError();
