@@ -225,7 +225,7 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
             const char* x = static_cast<const char*>(a.x) + r * a.xstride * EB;
 #pragma unroll
             for (int u = 0; u < UPT; ++u)
-                raw[k][u] = ld_unit<EB>(x + offset_here(at[u].at * EB));
+                raw[k][u] = ld_unit<EB, true>(x + offset_here(at[u].at * EB));
         }
     };
 #pragma unroll
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
 #pragma unroll
                 for (int j = 0; j < E; ++j)
                     v[j] = __builtin_fmaf((v[j] - mean[k]) * rstd, w[u][j], b[u][j]);
-                st_place<EB, RAGGED, true>(y, at[u], Vec<EB>::pack(v));
+                st_place<EB, RAGGED>(y, at[u], Vec<EB>::pack(v));
             }
             if (threadIdx.x == 0) {
                 a.mean[r0 + k] = mean[k];
