@@ -405,22 +405,38 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
 struct RowSums {
     float m[16], s[16], tm[16], ts[16], loss[16];
 };
-template <int EB, int IB, int UPT>
+// What a launch of the row kernel computes: loss and gradient, the gradient from
+// a given lse, or loss and lse.
+enum RowPass { PASS_STEP, PASS_BACKWARD, PASS_LOSS };
+
+// Entries of a row in LDS, rounded up so that four are read at a time.
+__host__ __device__ inline int padded(int top) { return (top + 3) & ~3; }
+
+// FULL: every wavefront has lanes in each of its UPT units, and spends no branch
+// on asking (4096 x 131072 bf16 407 us against 424).
+template <int EB, int IB, int UPT, RowPass PASS, bool FULL>
 __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     constexpr int E = Vec<EB>::E;
     constexpr uint32_t kNinf = EB == 2 ? 0xff80ff80u : 0xff800000u;
+    constexpr bool kSums = PASS != PASS_BACKWARD, kGrad = PASS != PASS_LOSS;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    extern __shared__ i32x4 entries[];   // places, then teacher logits, of two rows
     __shared__ RowSums red[2];
-    __shared__ int at[2][kMaxTop];
-    __shared__ float tz[2][kMaxTop];
     const int nt = blockDim.x, waves = nt >> 6, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int top = (int)a.top, tid = threadIdx.x;
-    const float c = kLog2e / a.temperature;
+    const int top = (int)a.top, tid = threadIdx.x, pad = padded(top);
+    int* const at = reinterpret_cast<int*>(entries);
+    float* const tz = reinterpret_cast<float*>(at + 2 * pad);
+    const float c = kLog2e / a.temperature, it = 1.0f / a.temperature;
     u32x4 raw[UPT];
     // (worked out where it is used: kept, the masks of all units would take
     // more scalar registers than there are)
     const auto place = [&](int u) {
         return place_unit<E>((u * nt + offset_here(threadIdx.x)) * E, (unsigned)a.vocab);
     };
+    // whether a unit is any lane's of this wavefront
+    const int units = ((int)a.vocab + E - 1) / E;
+    const int lane0 = __builtin_amdgcn_readfirstlane(tid);
+    const auto live = [&](int u) { return FULL || u * nt + lane0 < units; };
     const auto logit = [&](size_t r, int v) {
         return Vec<EB>::ld1(static_cast<const char*>(a.logits) + (r * a.lstride + v) * EB);
     };
@@ -440,20 +456,24 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     {
         const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
 #pragma unroll
-        for (int u = 0; u < UPT; ++u) raw[u] = ld_unit<EB, true>(z + place(u).at * EB);
+        for (int u = 0; u < UPT; ++u) {
+            raw[u] = u32x4{0u, 0u, 0u, 0u};
+            if (live(u)) raw[u] = ld_unit<EB, true>(z + place(u).at * EB);
+        }
     }
     const auto stage = [&](size_t row, int b) {
         if (tid < top) {
             my_t = my_at >= 0 ? my_t : -INFINITY;
-            at[b][tid] = my_at;
-            tz[b][tid] = my_t;
+            at[b * pad + tid] = my_at;
+            tz[b * pad + tid] = my_t;
         }
         for (int j = tid + nt; j < top; j += nt) {
             float x;
             const int v = entry(row, j, &x);
-            at[b][j] = v;
-            tz[b][j] = v >= 0 ? x : -INFINITY;
+            at[b * pad + j] = v;
+            tz[b * pad + j] = v >= 0 ? x : -INFINITY;
         }
+        if (tid < pad - top) at[b * pad + top + tid] = -2;   // (no place's)
     };
     stage(r, 0);
 
@@ -464,8 +484,8 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     int b = 0;
     bool some_before = false;
     const auto settle_row = [&](size_t row, int rb) {
-        if (owed) Vec<EB>::st1(owed_at, owed_v);
-        if (tid == 0) {
+        if (kGrad && owed) Vec<EB>::st1(owed_at, owed_v);
+        if (kSums && tid == 0) {
             float sum = 0.0f;
             for (int w = 0; w < waves; ++w) sum += red[rb].loss[w];
             a.loss[row] = some_before ? sum * (a.temperature * a.temperature) : 0.0f;
@@ -473,23 +493,28 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     };
 
     for (; r < a.rows; r += gridDim.x, b ^= 1) {
+        const int* const row_at = at + b * pad;
+        const float* const row_tz = tz + b * pad;
         // this wavefront's share of both sums
         Soft zs = soft_zero(), ts = soft_zero();
-        constexpr int G = UPT < 4 ? UPT : 4;
+        if constexpr (kSums) {
+            constexpr int G = UPT < 4 ? UPT : 4;
 #pragma unroll
-        for (int u = 0; u < UPT; u += G) {
+            for (int u = 0; u < UPT; u += G) {
+                if (!live(u)) continue;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int skip = place(u + g).skip;
-                if (skip) raw[u + g] = fill_first<EB>(raw[u + g], skip, kNinf);
+                for (int g = 0; g < G; ++g) {
+                    const int skip = place(u + g).skip;
+                    if (skip) raw[u + g] = fill_first<EB>(raw[u + g], skip, kNinf);
+                }
+                soft_units<EB, G>(zs, raw + u, c);
             }
-            soft_units<EB, G>(zs, raw + u, c);
+            zs = wave_soft(zs, c);
         }
         for (int j = tid; j < top; j += nt) {
-            const float one[1] = {tz[b][j]};
+            const float one[1] = {row_tz[j]};
             soft_add<1>(ts, one, c);
         }
-        zs = wave_soft(zs, c);
         ts = wave_soft(ts, c);
         if (lane == 0) {
             red[b].m[wave] = zs.m;
@@ -501,92 +526,120 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
         if (r >= gridDim.x) settle_row(r - gridDim.x, b ^ 1);
         const bool has = lane < waves;
         const int w = lane & 15;
-        zs = wave_soft({has ? red[b].m[w] : -INFINITY, has ? red[b].s[w] : 0.0f}, c);
+        if constexpr (kSums)
+            zs = wave_soft({has ? red[b].m[w] : -INFINITY, has ? red[b].s[w] : 0.0f}, c);
         ts = wave_soft({has ? red[b].tm[w] : -INFINITY, has ? red[b].ts[w] : 0.0f}, c);
         const bool some = !(ts.s == 0.0f);
-        const float scale = a.dloss[r] * a.temperature;
-        const float base = soft_base(zs.m), logz = logf(zs.s);
+        const float scale = kGrad ? a.dloss[r] * a.temperature : 0.0f;
+        const float base = soft_base(zs.m), logz = logf(zs.s), inv = 1.0f / zs.s;
+        const float lse = kSums ? 0.0f : a.lse_in[r];
         const float tbase = soft_base(ts.m), logs = logf(ts.s), tinv = 1.0f / ts.s;
         char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;
+        if (PASS == PASS_LOSS && tid == 0) a.lse[r] = soft_lse(zs, a.temperature);
 
         // loss terms, and the value that an entry's place gets
-        const auto prob = [&](int j) { return exp2_fast((tz[b][j] - tbase) * c) * tinv; };
+        const auto prob = [&](int j) { return exp2_fast((row_tz[j] - tbase) * c) * tinv; };
+        const auto student = [&](float zj) {
+            if constexpr (kSums) return exp2_fast((zj - base) * c) * inv;
+            else return expf(__builtin_fmaf(zj, it, -lse));
+        };
         const auto term = [&](int j, float zj) {
             const float p = prob(j);
-            if (at[b][j] < 0 || p == 0.0f) return 0.0f;
-            return p * ((tz[b][j] - tbase) / a.temperature - logs -
+            if (row_at[j] < 0 || p == 0.0f) return 0.0f;
+            return p * ((row_tz[j] - tbase) / a.temperature - logs -
                         ((zj - base) / a.temperature - logz));
         };
         const auto patch = [&](int j, float zj, float* v) {
-            const int mine = at[b][j];
-            float p = 0.0f;
-            bool first = mine >= 0;
-            for (int k = 0; k < top; ++k)
-                if (at[b][k] == mine) {
-                    first &= k >= j;
-                    p += prob(k);
+            const int mine = row_at[j];
+            if (mine < 0) return false;
+            const i32x4* const quads = reinterpret_cast<const i32x4*>(row_at);
+            int same = 0, before = 0;
+#pragma unroll 4
+            for (int k = 0; k < pad; k += 4) {
+                const i32x4 q = quads[k >> 2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    same += q[i] == mine;
+                    before += q[i] == mine && k + i < j;
                 }
-            *v = (exp2_fast((zj - base) * c) / zs.s - p) * scale;
-            return first;
+            }
+            float p = 0.0f;
+            if (same == 1) p = prob(j);
+            else   // named more than once: every entry adds the same ones in the same order
+                for (int k = 0; k < top; ++k)
+                    if (row_at[k] == mine) p += prob(k);
+            *v = (student(zj) - p) * scale;
+            return before == 0;
         };
         float loss = 0.0f;
         owed = false;
         some_before = some;
         if (some) {
             if (tid < top) {
-                loss = term(tid, my_z);
-                owed = patch(tid, my_z, &owed_v);
-                owed_at = dz + (size_t)(my_at < 0 ? 0 : my_at) * EB;
+                if constexpr (kSums) loss = term(tid, my_z);
+                if constexpr (kGrad) {
+                    owed = patch(tid, my_z, &owed_v);
+                    owed_at = dz + (size_t)(my_at < 0 ? 0 : my_at) * EB;
+                }
             }
-            for (int j = tid + nt; j < top; j += nt)
-                if (at[b][j] >= 0) loss += term(j, logit(r, at[b][j]));
+            if constexpr (kSums)
+                for (int j = tid + nt; j < top; j += nt)
+                    if (row_at[j] >= 0) loss += term(j, logit(r, row_at[j]));
         }
-        loss = wave_sum(loss);
-        if (lane == 0) red[b].loss[wave] = loss;
+        if constexpr (kSums) {
+            loss = wave_sum(loss);
+            if (lane == 0) red[b].loss[wave] = loss;
+        }
 
         // the row's gradient; the next row's units take the registers
         const bool more = r + gridDim.x < a.rows;
         const size_t next = r + gridDim.x;
         const char* zn = static_cast<const char*>(a.logits) + next * a.lstride * EB;
         if (more && tid < top) my_at = entry(next, tid, &my_t);
-        const float gain = scale / zs.s, bias = log2f(fabsf(gain));
+        const float gain = scale * inv, lift = log2f(fabsf(kSums ? gain : scale));
         const uint32_t sign = as_u32(scale) & 0x80000000u, sign2 = sign | (sign >> 16);
 #pragma unroll
         for (int u = 0; u < UPT; ++u) {
-            u32x4 out = {0u, 0u, 0u, 0u};
-            refresh(raw[u]);
-            if (some) {
-                float v[E];
-                Vec<EB>::unpack(raw[u], v);
-                if constexpr (EB == 2) {
-                    // |gain| goes into the exponent, where fp32 still holds
-                    // 2^-18 of a value: bf16 rounds at 2^-8
-#pragma unroll
-                    for (int j = 0; j < E; ++j)
-                        v[j] = exp2_fast(__builtin_fmaf(v[j] - base, c, bias));
-                    out = Vec<EB>::pack(v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) out[i] ^= sign2;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < E; ++j)
-                        v[j] = exp2_fast((v[j] - base) * c) * gain;
-                    out = Vec<EB>::pack(v);
-                }
-            }
-            const Place pl = place(u);
-            st_place<EB, true, true>(dz, pl, out);
-            if (more) raw[u] = ld_unit<EB, true>(zn + pl.at * EB);
             if (u == UPT / 2 && more && tid < top && my_at >= 0) my_z = logit(next, my_at);
+            if (!live(u)) continue;
+            const Place pl = place(u);
+            if constexpr (kGrad) {
+                u32x4 out = {0u, 0u, 0u, 0u};
+                refresh(raw[u]);
+                if (some) {
+                    float v[E];
+                    Vec<EB>::unpack(raw[u], v);
+                    if constexpr (EB == 2) {
+                        // the factor goes into the exponent, where fp32 still
+                        // holds 2^-18 of a value: bf16 rounds at 2^-8
+#pragma unroll
+                        for (int j = 0; j < E; ++j)
+                            v[j] = kSums ? exp2_fast(__builtin_fmaf(v[j] - base, c, lift))
+                                         : exp2_fast(__builtin_fmaf(
+                                               __builtin_fmaf(v[j], it, -lse), kLog2e, lift));
+                        out = Vec<EB>::pack(v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) out[i] ^= sign2;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < E; ++j)
+                            v[j] = kSums ? exp2_fast((v[j] - base) * c) * gain
+                                         : expf(__builtin_fmaf(v[j], it, -lse)) * scale;
+                        out = Vec<EB>::pack(v);
+                    }
+                }
+                st_place<EB, true, true>(dz, pl, out);
+            }
+            if (more) raw[u] = ld_unit<EB, true>(zn + pl.at * EB);
         }
         if (more) stage(next, b ^ 1);
-        if (top > nt) {   // the entries beyond this thread's first
+        if (kGrad && top > nt) {   // the entries beyond this thread's first
             __syncthreads();
             for (int j = tid + nt; some && j < top; j += nt)
-                if (at[b][j] >= 0) {
+                if (row_at[j] >= 0) {
                     float v;
-                    if (patch(j, logit(r, at[b][j]), &v))
-                        Vec<EB>::st1(dz + (size_t)at[b][j] * EB, v);
+                    if (patch(j, logit(r, row_at[j]), &v))
+                        Vec<EB>::st1(dz + (size_t)row_at[j] * EB, v);
                 }
         }
     }
@@ -595,7 +648,8 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
 }
 
 // The split of rows into chunks of UPT units a thread: 8, or 2 where there are
-// too few chunks of 8 for the card's compute units.
+// too few chunks of 8 for the card's compute units or rows fill less than half
+// of one.
 struct Split {
     int upt;
     size_t parts;
@@ -603,7 +657,7 @@ struct Split {
 Split split_of(size_t rows, size_t vocab, int eb) {
     const size_t e = 16 / (size_t)eb, units = (vocab + e - 1) / e;
     const size_t parts = (units + 8 * kThreads - 1) / (8 * kThreads);
-    if (rows * parts >= 1024) return {8, parts};
+    if (rows * parts >= 1024 && units > 4 * kThreads) return {8, parts};
     return {2, (units + 2 * kThreads - 1) / (2 * kThreads)};
 }
 
@@ -615,16 +669,27 @@ constexpr int kCUs = 256;
 struct RowFit {
     int upt, threads;
 };
+// (Above 256 threads in steps of 256, so that a compute unit's four SIMDs get
+// the same number of wavefronts: 2047 x 50021 bf16 103 us, with the 13
+// wavefronts that it takes instead of 16 126 us.)
 RowFit row_fit(size_t rows, size_t vocab, int eb) {
-    const size_t e = 16 / eb, units = (vocab + e - 1) / e;
-    if (vocab < e) return {0, 0};
-    for (int upt = 16; upt >= 4; upt /= 2) {
-        const size_t nt = (((units + upt - 1) / upt) + 63) / 64 * 64;
-        if (nt > 1024) break;
-        if (upt == 4 || rows * nt >= (size_t)kCUs * 1024) return {upt, (int)nt};
-        if ((((units + upt / 2 - 1) / (upt / 2)) + 63) / 64 * 64 > 1024) return {upt, (int)nt};
-    }
-    return {0, 0};
+    const size_t e = 16 / (size_t)eb, units = (vocab + e - 1) / e;
+    const auto threads = [&](size_t upt) {
+        const size_t nt = (units + upt - 1) / upt, step = nt > 256 ? 256 : 64;
+        return (nt + step - 1) / step * step;
+    };
+    if (vocab < e || threads(16) > 1024) return {0, 0};
+    int upt = 16;
+    while (upt > 4 && rows * threads(upt) < (size_t)kCUs * 1024 && threads(upt / 2) <= 1024)
+        upt /= 2;
+    return {upt, (int)threads(upt)};
+}
+// Few long rows leave most compute units without one: two passes over chunks
+// (1 x 131072 bf16 11.6 us against 17.3, 64 x 100000 18.3 against 19.5; 1 x
+// 32000 is better off in one launch, 8.4 against 11.9).
+RowFit step_fit(size_t rows, size_t vocab, int eb) {
+    const RowFit fit = row_fit(rows, vocab, eb);
+    return rows <= 64 && fit.upt * fit.threads > 4096 ? RowFit{0, 0} : fit;
 }
 
 unsigned grid_of(size_t tasks) {
@@ -673,8 +738,36 @@ hipError_t launch_grad(const DistillArgs& a, Split sp, hipStream_t s) {
     return hipGetLastError();
 }
 
-// From this many rows on the loss takes a block per row and one launch.
+template <RowPass PASS>
+hipError_t launch_rows(const DistillArgs& a, RowFit fit, hipStream_t s) {
+    // as many blocks as run at once: the registers of 4 units a thread leave
+    // room for 24 wavefronts a compute unit, the others' for 16
+    const size_t most = (size_t)kCUs * (fit.upt == 4 ? 1536 : 1024) / fit.threads;
+    const dim3 grid((unsigned)(a.rows < most ? a.rows : most)), block(fit.threads);
+    const size_t lds = (size_t)padded((int)a.top) * 4 * sizeof(float);
+    const size_t e = 16 / (size_t)a.eb, units = (a.vocab + e - 1) / e;
+    const bool full = PASS == PASS_STEP && units + 63 >= (size_t)fit.threads * 16;
+#define LAUNCH(EB, IB, UPT, FULL) \
+    hipLaunchKernelGGL((k_distill_rows<EB, IB, UPT, PASS, FULL>), grid, block, lds, s, a)
+#define CALL(EB, IB)                                                                    \
+    if (fit.upt == 4) LAUNCH(EB, IB, 4, false);                                         \
+    else if (fit.upt == 8) LAUNCH(EB, IB, 8, false);                                    \
+    else if (full) LAUNCH(EB, IB, 16, PASS == PASS_STEP);                               \
+    else LAUNCH(EB, IB, 16, false)
+    DISTILL_BY_TYPE(CALL);
+#undef CALL
+#undef LAUNCH
+    return hipGetLastError();
+}
+
+// From this many rows on the loss takes a block per row and one launch.  Rows
+// of up to kRowUnits units take the row kernel for the loss and for the
+// gradient too (7698 x 1856 fp32 loss 19 us against 27, 2047 x 8001 bf16
+// gradient 21 against 30); longer ones, whose pass has no use for the whole row
+// at once, are faster in chunks (2047 x 50021 fp32 loss 73 against 100,
+// gradient 164 against 176).
 constexpr size_t kLossRows = 512;
+constexpr int kRowUnits = 4096;
 bool loss_by_rows(size_t rows, size_t vocab, int eb) {
     return rows >= kLossRows && vocab >= (size_t)(16 / eb);
 }
@@ -682,7 +775,7 @@ bool loss_by_rows(size_t rows, size_t vocab, int eb) {
 }  // namespace
 
 size_t distill_work_floats(size_t rows, size_t vocab, int eb, bool step) {
-    if (rows == 0 || (step ? row_fit(rows, vocab, eb).upt != 0 : loss_by_rows(rows, vocab, eb)))
+    if (rows == 0 || (step ? step_fit(rows, vocab, eb).upt != 0 : loss_by_rows(rows, vocab, eb)))
         return 0;
     return 2 * rows * split_of(rows, vocab, eb).parts;
 }
@@ -691,6 +784,8 @@ hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
     const dim3 grid(grid_of(a.rows)), block(kThreads);
     if (loss_by_rows(a.rows, a.vocab, a.eb)) {
+        const RowFit fit = row_fit(a.rows, a.vocab, a.eb);
+        if (fit.upt && fit.threads * fit.upt <= kRowUnits) return launch_rows<PASS_LOSS>(a, fit, s);
 #define CALL(EB, IB) hipLaunchKernelGGL((k_distill_loss_rows<EB, IB>), grid, block, 0, s, a)
         DISTILL_BY_TYPE(CALL);
 #undef CALL
@@ -707,24 +802,16 @@ hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s) {
 
 hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
+    const RowFit fit = row_fit(a.rows, a.vocab, a.eb);
+    if (fit.upt && fit.threads * fit.upt <= kRowUnits && a.rows >= kLossRows)
+        return launch_rows<PASS_BACKWARD>(a, fit, s);
     return launch_grad<false>(a, split_of(a.rows, a.vocab, a.eb), s);
 }
 
 hipError_t launch_distill_step(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    const RowFit fit = row_fit(a.rows, a.vocab, a.eb);
-    if (fit.upt) {
-        // as many blocks as run at once: 16 wavefronts a compute unit
-        const size_t most = (size_t)kCUs * 1024 / fit.threads;
-        const dim3 grid((unsigned)(a.rows < most ? a.rows : most)), block(fit.threads);
-#define CALL(EB, IB)                                                                             \
-    if (fit.upt == 4) hipLaunchKernelGGL((k_distill_rows<EB, IB, 4>), grid, block, 0, s, a);     \
-    else if (fit.upt == 8) hipLaunchKernelGGL((k_distill_rows<EB, IB, 8>), grid, block, 0, s, a); \
-    else hipLaunchKernelGGL((k_distill_rows<EB, IB, 16>), grid, block, 0, s, a)
-        DISTILL_BY_TYPE(CALL);
-#undef CALL
-        return hipGetLastError();
-    }
+    const RowFit fit = step_fit(a.rows, a.vocab, a.eb);
+    if (fit.upt) return launch_rows<PASS_STEP>(a, fit, s);
     const Split sp = split_of(a.rows, a.vocab, a.eb);
     const hipError_t e = launch_part(a, sp, s);
     return e != hipSuccess ? e : launch_grad<true>(a, sp, s);
