@@ -552,7 +552,7 @@ ar_status ar_distill_step(ar_ctx* ctx, const float* dloss, const void* logits,
                           const void* teacher, size_t rows, size_t vocab, size_t top,
                           ar_dtype dtype, float temperature, float* loss, void* dlogits,
                           void* workspace, size_t workspace_bytes);
-ar_status ar_distill_workspace(size_t rows, size_t vocab, ar_dtype dtype, int gradient,
+ar_status ar_distill_workspace(size_t rows, size_t vocab, size_t top, ar_dtype dtype, int gradient,
                                size_t* bytes);
 
 /* Static description of a status code (never NULL). */

@@ -112,7 +112,7 @@ def _load() -> ctypes.CDLL:
         "ar_distill_loss": ([vp, vp, sz, vp, i, vp, sz, sz, sz, i, f, vp, vp, vp, sz], i),
         "ar_distill_backward": ([vp, vp, vp, sz, vp, i, vp, vp, sz, sz, sz, i, f, vp], i),
         "ar_distill_step": ([vp, vp, vp, sz, vp, i, vp, sz, sz, sz, i, f, vp, vp, vp, sz], i),
-        "ar_distill_workspace": ([sz, sz, i, i, psz], i),
+        "ar_distill_workspace": ([sz, sz, sz, i, i, psz], i),
         "ar_status_string": ([i], cp),
         "ar_last_error": ([vp], cp),
         "ar_destroy": ([vp], i),

@@ -36,9 +36,34 @@ __device__ __forceinline__ int place_of(const void* indices, size_t j, size_t vo
     }
 }
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+// Entries of a row in LDS, rounded up so that four are read at a time; the
+// places past the last are kNoPlace.
+__host__ __device__ inline int padded(int top) { return (top + 3) & ~3; }
+constexpr int kNoPlace = -2;
+
+// How many of the row's entries name entry j's place, and how many of them
+// before it.
+__device__ __forceinline__ void count_same(const int* at, int pad, int j, int* same, int* before) {
+    const i32x4* const quads = reinterpret_cast<const i32x4*>(at);
+    const int mine = at[j];
+    int s = 0, b = 0;
+#pragma unroll 4
+    for (int k = 0; k < pad; k += 4) {
+        const i32x4 q = quads[k >> 2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s += q[i] == mine;
+            b += q[i] == mine && k + i < j;
+        }
+    }
+    *same = s;
+    *before = b;
+}
+
 // The teacher of one row in LDS: places (-1: left out) and probabilities.
 struct Teacher {
-    int at[kMaxTop];
+    alignas(16) int at[kMaxTop];
     float p[kMaxTop];
     float red[2][16];
 };
@@ -70,6 +95,7 @@ __device__ bool load_teacher(const DistillArgs& a, size_t r, Teacher& th, float*
         th.p[j] = z;
         m = z != z ? z : fmaxf(m, z);   // (a NaN reaches the sum below by itself)
     }
+    if ((int)threadIdx.x < padded((int)a.top) - (int)a.top) th.at[a.top + threadIdx.x] = kNoPlace;
     m = block_max<W>(m == m ? m : -INFINITY, th.red[0]);
     const float base = m == -INFINITY ? 0.0f : m;
     float s = 0.0f;
@@ -374,17 +400,14 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
             for (int j = threadIdx.x; j < (int)a.top; j += kThreads) {
                 const int at = th.at[j];
                 if (at < 0 || (unsigned)at < from || (unsigned)at >= to) continue;
-                float p = 0.0f;
-                bool mine = true;
-                for (int k = 0; k < (int)a.top; ++k)
-                    if (th.at[k] == at) {
-                        mine &= k >= j;
-                        p += th.p[k];
-                    }
-                if (mine) {
-                    const float q = prob(Vec<EB>::ld1(z + (size_t)at * EB));
-                    Vec<EB>::st1(dz + (size_t)at * EB, (q - p) * scale);
-                }
+                int same, before;
+                count_same(th.at, padded((int)a.top), j, &same, &before);
+                if (before) continue;
+                float p = th.p[j];
+                for (int k = j + 1; same > 1 && k < (int)a.top; ++k)
+                    if (th.at[k] == at) p += th.p[k];
+                const float q = prob(Vec<EB>::ld1(z + (size_t)at * EB));
+                Vec<EB>::st1(dz + (size_t)at * EB, (q - p) * scale);
             }
         __syncthreads();
     }
@@ -396,9 +419,8 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
 // that loads, exponentials and stores of one compute unit overlap although a
 // row may fill most of its registers.
 //
-// Thread j keeps teacher entry j of the row (and, in blocks of fewer threads
-// than entries, walks the others); the next row's entries are loaded among its
-// units.  There is one barrier a row: before it every wavefront leaves its sums
+// Thread j keeps teacher entry j of the row (a block has a thread for each); the
+// next row's entries are loaded among its units.  There is one barrier a row: before it every wavefront leaves its sums
 // of this row, after it the entries' places of the row before are written again
 // with q - p (its plain gradients were all stored before the barrier) and its
 // loss is added up.  What one row leaves in LDS the next but one replaces.
@@ -409,9 +431,6 @@ struct RowSums {
 // a given lse, or loss and lse.
 enum RowPass { PASS_STEP, PASS_BACKWARD, PASS_LOSS };
 
-// Entries of a row in LDS, rounded up so that four are read at a time.
-__host__ __device__ inline int padded(int top) { return (top + 3) & ~3; }
-
 // FULL: every wavefront has lanes in each of its UPT units, and spends no branch
 // on asking (4096 x 131072 bf16 407 us against 424).
 template <int EB, int IB, int UPT, RowPass PASS, bool FULL>
@@ -419,7 +438,6 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     constexpr int E = Vec<EB>::E;
     constexpr uint32_t kNinf = EB == 2 ? 0xff80ff80u : 0xff800000u;
     constexpr bool kSums = PASS != PASS_BACKWARD, kGrad = PASS != PASS_LOSS;
-    typedef int i32x4 __attribute__((ext_vector_type(4)));
     extern __shared__ i32x4 entries[];   // places, then teacher logits, of two rows
     __shared__ RowSums red[2];
     const int nt = blockDim.x, waves = nt >> 6, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -461,21 +479,15 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
             if (live(u)) raw[u] = ld_unit<EB, true>(z + place(u).at * EB);
         }
     }
-    const auto stage = [&](size_t row, int b) {
+    const auto stage = [&](int b) {
         if (tid < top) {
             my_t = my_at >= 0 ? my_t : -INFINITY;
             at[b * pad + tid] = my_at;
             tz[b * pad + tid] = my_t;
         }
-        for (int j = tid + nt; j < top; j += nt) {
-            float x;
-            const int v = entry(row, j, &x);
-            at[b * pad + j] = v;
-            tz[b * pad + j] = v >= 0 ? x : -INFINITY;
-        }
-        if (tid < pad - top) at[b * pad + top + tid] = -2;   // (no place's)
+        if (tid < pad - top) at[b * pad + top + tid] = kNoPlace;
     };
-    stage(r, 0);
+    stage(0);
 
     // the entry of the row before that is still to be written, and its loss
     bool owed = false;
@@ -511,8 +523,8 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
             }
             zs = wave_soft(zs, c);
         }
-        for (int j = tid; j < top; j += nt) {
-            const float one[1] = {row_tz[j]};
+        if (tid < top) {
+            const float one[1] = {my_t};
             soft_add<1>(ts, one, c);
         }
         ts = wave_soft(ts, c);
@@ -543,48 +555,24 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
             if constexpr (kSums) return exp2_fast((zj - base) * c) * inv;
             else return expf(__builtin_fmaf(zj, it, -lse));
         };
-        const auto term = [&](int j, float zj) {
-            const float p = prob(j);
-            if (row_at[j] < 0 || p == 0.0f) return 0.0f;
-            return p * ((row_tz[j] - tbase) / a.temperature - logs -
-                        ((zj - base) / a.temperature - logz));
-        };
-        const auto patch = [&](int j, float zj, float* v) {
-            const int mine = row_at[j];
-            if (mine < 0) return false;
-            const i32x4* const quads = reinterpret_cast<const i32x4*>(row_at);
-            int same = 0, before = 0;
-#pragma unroll 4
-            for (int k = 0; k < pad; k += 4) {
-                const i32x4 q = quads[k >> 2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    same += q[i] == mine;
-                    before += q[i] == mine && k + i < j;
-                }
-            }
-            float p = 0.0f;
-            if (same == 1) p = prob(j);
-            else   // named more than once: every entry adds the same ones in the same order
-                for (int k = 0; k < top; ++k)
-                    if (row_at[k] == mine) p += prob(k);
-            *v = (student(zj) - p) * scale;
-            return before == 0;
-        };
         float loss = 0.0f;
         owed = false;
         some_before = some;
-        if (some) {
-            if (tid < top) {
-                if constexpr (kSums) loss = term(tid, my_z);
-                if constexpr (kGrad) {
-                    owed = patch(tid, my_z, &owed_v);
-                    owed_at = dz + (size_t)(my_at < 0 ? 0 : my_at) * EB;
-                }
+        if (some && tid < top && my_at >= 0) {
+            const float p = prob(tid);
+            if (kSums && p != 0.0f)
+                loss = p * ((my_t - tbase) / a.temperature - logs -
+                            ((my_z - base) / a.temperature - logz));
+            if constexpr (kGrad) {
+                int same, before;
+                count_same(row_at, pad, tid, &same, &before);
+                float all = p;
+                for (int k = tid + 1; same > 1 && k < top; ++k)
+                    if (row_at[k] == my_at) all += prob(k);
+                owed = before == 0;
+                owed_at = dz + (size_t)my_at * EB;
+                owed_v = (student(my_z) - all) * scale;
             }
-            if constexpr (kSums)
-                for (int j = tid + nt; j < top; j += nt)
-                    if (row_at[j] >= 0) loss += term(j, logit(r, row_at[j]));
         }
         if constexpr (kSums) {
             loss = wave_sum(loss);
@@ -632,16 +620,7 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
             }
             if (more) raw[u] = ld_unit<EB, true>(zn + pl.at * EB);
         }
-        if (more) stage(next, b ^ 1);
-        if (kGrad && top > nt) {   // the entries beyond this thread's first
-            __syncthreads();
-            for (int j = tid + nt; some && j < top; j += nt)
-                if (row_at[j] >= 0) {
-                    float v;
-                    if (patch(j, logit(r, row_at[j]), &v))
-                        Vec<EB>::st1(dz + (size_t)row_at[j] * EB, v);
-                }
-        }
+        if (more) stage(b ^ 1);
     }
     __syncthreads();
     if (r >= gridDim.x) settle_row(r - gridDim.x, b ^ 1);
@@ -672,23 +651,25 @@ struct RowFit {
 // (Above 256 threads in steps of 256, so that a compute unit's four SIMDs get
 // the same number of wavefronts: 2047 x 50021 bf16 103 us, with the 13
 // wavefronts that it takes instead of 16 126 us.)
-RowFit row_fit(size_t rows, size_t vocab, int eb) {
+RowFit row_fit(size_t rows, size_t vocab, size_t top, int eb) {
     const size_t e = 16 / (size_t)eb, units = (vocab + e - 1) / e;
     const auto threads = [&](size_t upt) {
-        const size_t nt = (units + upt - 1) / upt, step = nt > 256 ? 256 : 64;
+        const size_t need = (units + upt - 1) / upt, nt = need > top ? need : top;
+        const size_t step = nt > 256 ? 256 : 64;
         return (nt + step - 1) / step * step;
     };
     if (vocab < e || threads(16) > 1024) return {0, 0};
     int upt = 16;
-    while (upt > 4 && rows * threads(upt) < (size_t)kCUs * 1024 && threads(upt / 2) <= 1024)
+    while (upt > 4 && threads(upt / 2) <= 1024 &&
+           (rows * threads(upt) < (size_t)kCUs * 1024 || threads(upt / 2) == threads(upt)))
         upt /= 2;
     return {upt, (int)threads(upt)};
 }
 // Few long rows leave most compute units without one: two passes over chunks
 // (1 x 131072 bf16 11.6 us against 17.3, 64 x 100000 18.3 against 19.5; 1 x
 // 32000 is better off in one launch, 8.4 against 11.9).
-RowFit step_fit(size_t rows, size_t vocab, int eb) {
-    const RowFit fit = row_fit(rows, vocab, eb);
+RowFit step_fit(size_t rows, size_t vocab, size_t top, int eb) {
+    const RowFit fit = row_fit(rows, vocab, top, eb);
     return rows <= 64 && fit.upt * fit.threads > 4096 ? RowFit{0, 0} : fit;
 }
 
@@ -774,8 +755,9 @@ bool loss_by_rows(size_t rows, size_t vocab, int eb) {
 
 }  // namespace
 
-size_t distill_work_floats(size_t rows, size_t vocab, int eb, bool step) {
-    if (rows == 0 || (step ? step_fit(rows, vocab, eb).upt != 0 : loss_by_rows(rows, vocab, eb)))
+size_t distill_work_floats(size_t rows, size_t vocab, size_t top, int eb, bool step) {
+    if (rows == 0 ||
+        (step ? step_fit(rows, vocab, top, eb).upt != 0 : loss_by_rows(rows, vocab, eb)))
         return 0;
     return 2 * rows * split_of(rows, vocab, eb).parts;
 }
@@ -784,7 +766,7 @@ hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
     const dim3 grid(grid_of(a.rows)), block(kThreads);
     if (loss_by_rows(a.rows, a.vocab, a.eb)) {
-        const RowFit fit = row_fit(a.rows, a.vocab, a.eb);
+        const RowFit fit = row_fit(a.rows, a.vocab, a.top, a.eb);
         if (fit.upt && fit.threads * fit.upt <= kRowUnits) return launch_rows<PASS_LOSS>(a, fit, s);
 #define CALL(EB, IB) hipLaunchKernelGGL((k_distill_loss_rows<EB, IB>), grid, block, 0, s, a)
         DISTILL_BY_TYPE(CALL);
@@ -802,7 +784,7 @@ hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s) {
 
 hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    const RowFit fit = row_fit(a.rows, a.vocab, a.eb);
+    const RowFit fit = row_fit(a.rows, a.vocab, a.top, a.eb);
     if (fit.upt && fit.threads * fit.upt <= kRowUnits && a.rows >= kLossRows)
         return launch_rows<PASS_BACKWARD>(a, fit, s);
     return launch_grad<false>(a, split_of(a.rows, a.vocab, a.eb), s);
@@ -810,7 +792,7 @@ hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s) {
 
 hipError_t launch_distill_step(const DistillArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    const RowFit fit = step_fit(a.rows, a.vocab, a.eb);
+    const RowFit fit = step_fit(a.rows, a.vocab, a.top, a.eb);
     if (fit.upt) return launch_rows<PASS_STEP>(a, fit, s);
     const Split sp = split_of(a.rows, a.vocab, a.eb);
     const hipError_t e = launch_part(a, sp, s);

@@ -100,7 +100,7 @@ struct DistillArgs {
     int eb, ib;
 };
 
-size_t distill_work_floats(size_t rows, size_t vocab, int eb, bool step);
+size_t distill_work_floats(size_t rows, size_t vocab, size_t top, int eb, bool step);
 hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t s);
 hipError_t launch_distill_backward(const DistillArgs& a, hipStream_t s);
 hipError_t launch_distill_step(const DistillArgs& a, hipStream_t s);

@@ -435,7 +435,7 @@ ar_status ar_distill_loss(ar_ctx* ctx, const void* logits, size_t logits_stride,
         arrays.out(loss, rows * sizeof(float), 4, "loss");
         arrays.out(lse, rows * sizeof(float), 4, "lse");
         s = workspace(ctx, arrays, workspace_, workspace_bytes,
-                      arlib::distill_work_floats(rows, vocab, d.eb, false) * sizeof(float));
+                      arlib::distill_work_floats(rows, vocab, top, d.eb, false) * sizeof(float));
         if (s == AR_OK) s = arrays.check();
         if (s != AR_OK) return s;
         d.loss = loss;
@@ -487,7 +487,7 @@ ar_status ar_distill_step(ar_ctx* ctx, const float* dloss, const void* logits,
         arrays.out(loss, rows * sizeof(float), 4, "loss");
         arrays.out(dlogits, bytes, (size_t)d.eb, "dlogits");
         s = workspace(ctx, arrays, workspace_, workspace_bytes,
-                      arlib::distill_work_floats(rows, vocab, d.eb, true) * sizeof(float));
+                      arlib::distill_work_floats(rows, vocab, top, d.eb, true) * sizeof(float));
         if (s == AR_OK) s = arrays.check();
         if (s != AR_OK) return s;
         d.dloss = dloss;
@@ -498,13 +498,15 @@ ar_status ar_distill_step(ar_ctx* ctx, const float* dloss, const void* logits,
     });
 }
 
-ar_status ar_distill_workspace(size_t rows, size_t vocab, ar_dtype dtype, int gradient,
+ar_status ar_distill_workspace(size_t rows, size_t vocab, size_t top, ar_dtype dtype, int gradient,
                                size_t* bytes) {
     const size_t eb = float_bytes((int)dtype);
     size_t all;
-    if (!bytes || !eb || vocab < 1 || !times(vocab, eb, &all) || !times(all, rows, &all))
+    if (!bytes || !eb || vocab < 1 || top < 1 || !times(vocab, eb, &all) ||
+        !times(all, rows, &all))
         return AR_ERR_INVALID_ARG;
-    *bytes = arlib::distill_work_floats(rows, vocab, (int)eb, gradient != 0) * sizeof(float);
+    if (vocab > kMostCols || top > AR_DISTILL_MAX_TOP) return AR_ERR_UNSUPPORTED;
+    *bytes = arlib::distill_work_floats(rows, vocab, top, (int)eb, gradient != 0) * sizeof(float);
     return AR_OK;
 }
 

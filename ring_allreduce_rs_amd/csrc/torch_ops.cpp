@@ -468,8 +468,8 @@ struct Distill {
     }
     size_t workspace(int gradient) const {
         size_t bytes = 0;
-        must(nullptr, ar_distill_workspace((size_t)rows, (size_t)vocab, dt, gradient, &bytes),
-             "ar_distill_workspace");
+        must(nullptr, ar_distill_workspace((size_t)rows, (size_t)vocab, (size_t)top, dt, gradient,
+                                           &bytes), "ar_distill_workspace");
         return bytes;
     }
 };

@@ -168,13 +168,15 @@ void route() {
 void distill() {
     size_t need = 0;
     for (int grad = 0; grad < 2; ++grad) {
-        CHECK(ar_distill_workspace(4, 1000, AR_FLOAT32, grad, &need) == AR_OK);
-        CHECK(ar_distill_workspace(4, 0, AR_FLOAT32, grad, &need) == AR_ERR_INVALID_ARG);
-        CHECK(ar_distill_workspace(4, 1000, AR_INT32, grad, &need) == AR_ERR_INVALID_ARG);
-        CHECK(ar_distill_workspace(SIZE_MAX, 1000, AR_FLOAT32, grad, &need) == AR_ERR_INVALID_ARG);
-        CHECK(ar_distill_workspace(4, 1000, AR_FLOAT32, grad, nullptr) == AR_ERR_INVALID_ARG);
+        CHECK(ar_distill_workspace(4, 1000, 16, AR_FLOAT32, grad, &need) == AR_OK);
+        CHECK(ar_distill_workspace(4, 0, 16, AR_FLOAT32, grad, &need) == AR_ERR_INVALID_ARG);
+        CHECK(ar_distill_workspace(4, 1000, 0, AR_FLOAT32, grad, &need) == AR_ERR_INVALID_ARG);
+        CHECK(ar_distill_workspace(4, 1000, 1025, AR_FLOAT32, grad, &need) == AR_ERR_UNSUPPORTED);
+        CHECK(ar_distill_workspace(4, 1000, 16, AR_INT32, grad, &need) == AR_ERR_INVALID_ARG);
+        CHECK(ar_distill_workspace(SIZE_MAX, 1000, 16, AR_FLOAT32, grad, &need) == AR_ERR_INVALID_ARG);
+        CHECK(ar_distill_workspace(4, 1000, 16, AR_FLOAT32, grad, nullptr) == AR_ERR_INVALID_ARG);
     }
-    CHECK(ar_distill_workspace(4, 1000, AR_FLOAT32, 0, &need) == AR_OK);
+    CHECK(ar_distill_workspace(4, 1000, 16, AR_FLOAT32, 0, &need) == AR_OK);
     const auto l = [&](size_t stride, int ib, size_t rows, size_t vocab, size_t top, int dt, float T,
                        float* lse, void* ws, size_t n) {
         return ar_distill_loss(ctx, at(0), stride, at(1), ib, at(2), rows, vocab, top, (ar_dtype)dt,
@@ -206,7 +208,7 @@ void distill() {
                                                     at<float>(4), 4, 1000, 16, AR_BFLOAT16, 1.0f, at(0)));
     REFUSED(AR_ERR_INVALID_ARG, ar_distill_backward(ctx, nullptr, at(0), 1000, at(1), 4, at(2),
                                                     at<float>(4), 4, 1000, 16, AR_BFLOAT16, 1.0f, at(5)));
-    CHECK(ar_distill_workspace(4, 1000, AR_BFLOAT16, 1, &need) == AR_OK);
+    CHECK(ar_distill_workspace(4, 1000, 16, AR_BFLOAT16, 1, &need) == AR_OK);
     RUNS(ar_distill_step(ctx, at<float>(3), at(0), 1000, at(1), 4, at(2), 4, 1000, 16, AR_BFLOAT16,
                          1.0f, at<float>(4), at(5), at(6), need));
     REFUSED(AR_ERR_INVALID_ARG,
@@ -258,7 +260,7 @@ hipError_t launch_combine_grad(const CombineArgs& a, hipStream_t) {
     ++g_launches;
     return hipSuccess;
 }
-size_t distill_work_floats(size_t rows, size_t, int, bool step) { return rows * (step ? 4 : 2); }
+size_t distill_work_floats(size_t rows, size_t, size_t, int, bool step) { return rows * (step ? 4 : 2); }
 hipError_t launch_distill_loss(const DistillArgs& a, hipStream_t) {
     g_distill = a;
     ++g_launches;
