@@ -78,7 +78,7 @@ struct CombineArgs {
     int eb;
 };
 
-size_t dispatch_work_ints(size_t slots, int experts);
+size_t dispatch_work_ints(size_t tokens, int topk, int experts);
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s);
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s);
 hipError_t launch_combine_grad(const CombineArgs& a, hipStream_t s);

@@ -314,7 +314,7 @@ ar_status ar_expert_dispatch(ar_ctx* ctx, const void* x, size_t x_stride, const 
         arrays.out(slot, slots * sizeof(int), 4, "slot");
         arrays.out(offsets, ((size_t)experts + 1) * sizeof(int), 4, "offsets");
         s = workspace(ctx, arrays, workspace_, workspace_bytes,
-                      arlib::dispatch_work_ints(slots, experts) * sizeof(int));
+                      arlib::dispatch_work_ints(tokens, topk, experts) * sizeof(int));
         if (s == AR_OK) s = arrays.check();
         if (s != AR_OK) return s;
         arlib::DispatchArgs a{x,       ids,    rows,        dest, slot,    offsets,
@@ -329,7 +329,7 @@ ar_status ar_expert_dispatch_workspace(size_t tokens, int topk, int experts, siz
     if (!bytes || topk < 1 || experts < 1 || !times(tokens, (size_t)topk, &slots))
         return AR_ERR_INVALID_ARG;
     if (experts > AR_MAX_EXPERTS || slots > (size_t)INT_MAX) return AR_ERR_UNSUPPORTED;
-    *bytes = arlib::dispatch_work_ints(slots, experts) * sizeof(int);
+    *bytes = arlib::dispatch_work_ints(tokens, topk, experts) * sizeof(int);
     return AR_OK;
 }
 

@@ -251,8 +251,7 @@ __global__ __launch_bounds__(NT) void k_route_rows(const DispatchArgs a) {
 
 // The whole dispatch in one launch, for few slots: the last block counts the
 // experts' rows, every other block finds where its token's choices go by
-// comparing them with every slot, then copies.  (From kDirectSlots slots on the
-// comparisons cost more than the sort's launches.)
+// comparing them with every slot, then copies.
 template <int EB, int IB, int NT, RowMode MODE>
 __global__ __launch_bounds__(NT) void k_route_direct(const DispatchArgs a, int slots) {
     constexpr int W = NT / 64, KB = 8;
@@ -438,13 +437,23 @@ unsigned token_blocks(int tokens) {
     return (unsigned)(tokens < kMost ? tokens : kMost);
 }
 
-// Threads of a token's block: a row's units, at most 256.
-int token_threads(size_t hidden, int eb) {
+// Threads of a token's block: a row's units, at most 256, or 1024 while there
+// are fewer tokens than compute units (both gradients of 56 x 4 rows of 5742
+// fp32 11.7 us against 19.3 with 256).
+int token_threads(size_t tokens, size_t hidden, int eb) {
     const size_t units = (hidden * eb + 15) / 16;
-    return units <= 64 ? 64 : units <= 128 ? 128 : 256;
+    return units <= 64 ? 64 : units <= 128 ? 128 : units <= 256 || tokens > 256 ? 256 : 1024;
 }
 
-constexpr size_t kDirectSlots = 2048;
+// The direct form's comparisons: every token with every slot, 8 choices at a
+// time.  Up to kDirectWork of them it is one launch where the sort takes three
+// (652 x 5 slots 9.2 us against 12.7, 859 x 2 6.6 against 11.1; past it 1024 x 8
+// would take 19.5 against 16.5).
+constexpr size_t kDirectWork = size_t(1) << 25;
+bool direct_form(size_t tokens, size_t topk) {
+    const size_t slots = tokens * topk;
+    return slots <= 16384 && slots * tokens * ((topk + 7) / 8 * 8) <= kDirectWork;
+}
 
 // Rows of more bytes than this are read past the caches on the way back: they
 // would only push each other out of the 256 MB last-level cache (MI355X, rows
@@ -476,33 +485,46 @@ int sort_blocks(size_t slots) {
     do {                                    \
         if (nt == 64) BY_MODE(EB, 64, CALL); \
         else if (nt == 128) BY_MODE(EB, 128, CALL); \
-        else BY_MODE(EB, 256, CALL);        \
+        else if (nt == 256) BY_MODE(EB, 256, CALL); \
+        else BY_MODE(EB, 1024, CALL);       \
     } while (0)
 #define BY_ROW(CALL)                                        \
     do {                                                    \
-        const int nt = token_threads(a.hidden, a.eb);       \
+        const int nt = token_threads((size_t)a.tokens, a.hidden, a.eb); \
         const RowMode mode = row_mode(a.hidden, a.eb);      \
         if (a.eb == 2) BY_WIDTH(2, CALL);                   \
         else BY_WIDTH(4, CALL);                             \
     } while (0)
 
+// The direct form's blocks walk all slots, so they have 256 threads at least.
+#define BY_ROW_WIDE(CALL)                                                       \
+    do {                                                                        \
+        const int nt = token_threads((size_t)a.tokens, a.hidden, a.eb);         \
+        const RowMode mode = row_mode(a.hidden, a.eb);                          \
+        if (a.eb == 2 && nt <= 256) BY_MODE(2, 256, CALL);                      \
+        else if (a.eb == 2) BY_MODE(2, 1024, CALL);                             \
+        else if (nt <= 256) BY_MODE(4, 256, CALL);                              \
+        else BY_MODE(4, 1024, CALL);                                            \
+    } while (0)
+
 }  // namespace
 
-size_t dispatch_work_ints(size_t slots, int experts) {
-    if (slots <= kDirectSlots) return 0;
+size_t dispatch_work_ints(size_t tokens, int topk, int experts) {
+    const size_t slots = tokens * (size_t)topk;
+    if (direct_form(tokens, (size_t)topk)) return 0;
     return (size_t)sort_blocks(slots) * (size_t)(experts + 1);
 }
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
     const size_t slots = (size_t)a.tokens * a.topk;
-    if (slots <= kDirectSlots) {
+    if (direct_form((size_t)a.tokens, (size_t)a.topk)) {
         const dim3 grid(a.tokens + 1);
 #define CALL(EB, NT, MODE)                                                                    \
     if (a.ib == 8)                                                                            \
         hipLaunchKernelGGL((k_route_direct<EB, 8, NT, MODE>), grid, dim3(NT), 0, s, a, (int)slots); \
     else                                                                                      \
         hipLaunchKernelGGL((k_route_direct<EB, 4, NT, MODE>), grid, dim3(NT), 0, s, a, (int)slots)
-        BY_ROW(CALL);
+        BY_ROW_WIDE(CALL);
 #undef CALL
         return hipGetLastError();
     }

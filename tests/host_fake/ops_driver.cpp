@@ -244,7 +244,9 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t) {
     ++g_launches;
     return hipSuccess;
 }
-size_t dispatch_work_ints(size_t slots, int experts) { return (slots / 2048 + 1) * (experts + 1); }
+size_t dispatch_work_ints(size_t tokens, int topk, int experts) {
+    return (tokens * topk / 2048 + 1) * (experts + 1);
+}
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t) {
     g_dispatch = a;
     ++g_launches;

@@ -85,7 +85,7 @@ def test_one_expert_takes_all_or_none(tokens, topk):
         check_back(plan, 24, F32, 1)
 
 
-@pytest.mark.parametrize("slots", [4096, 40000 * 8, 70001 * 5])
+@pytest.mark.parametrize("slots", [4096, 1448 * 8, 20000, 40000 * 8, 70001 * 5])
 def test_many_slots(slots):
     """More slots than one round of the sort's blocks takes."""
     topk = 8 if slots % 8 == 0 else 5
