@@ -516,13 +516,17 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
                 if (!live(u)) continue;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    refresh(raw[u + g]);
+                    // (without a gradient to come back for, the compiler would
+                    // unpack the next row's units as they arrive and spill)
+                    if constexpr (!kGrad) refresh(raw[u + g]);
                     const int skip = place(u + g).skip;
                     if (skip) raw[u + g] = fill_first<EB>(raw[u + g], skip, kNinf);
                 }
                 soft_units<EB, G>(zs, raw + u, c);
-                settle(zs.m);
-                settle(zs.s);
+                if constexpr (!kGrad) {
+                    settle(zs.m);
+                    settle(zs.s);
+                }
             }
             zs = wave_soft(zs, c);
         }
