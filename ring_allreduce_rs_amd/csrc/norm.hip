@@ -9,6 +9,15 @@
 // All sums and statistics are fp32; each output is rounded once.  The variance
 // is taken from the centred values (a second pass over the row), so a mean far
 // larger than the spread costs no digits.
+//
+// Bound by HBM: 2 (3) bytes x element size an element against 8 (14) flops.  A
+// row stays in the registers of a block between its sums and its output, so x
+// (and dy) are read once.  A block rather than a wavefront a row: the parameters
+// are loaded once for R rows of a short share each (one wavefront with 8 units a
+// lane reads them for every row: 70 us at 16384 x 4096 bf16, against 47).
+// MI355X: forward 16384 x 4096 bf16 47.7 us (5.6 TB/s; a copy of as many bytes
+// 41.5), backward 8192 x 8192 bf16 with fp32 weights 79.6 us (5.1 TB/s; 62),
+// 1021 x 771 fp32 9.2 us, one row of 4096 5.5 us, of which the kernel is 2.6.
 #include <cmath>
 
 #include "ops.h"
@@ -299,7 +308,8 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
     }
 }
 
-// Both gradients in one pass over x and dy.  Each thread owns the same columns
+// Both gradients in one pass over x and dy (a second pass for the column sums
+// took 164 us in all at 8192 x 8192 bf16, this form 79.6).  Each thread owns the same columns
 // in every row that its block takes, so the column sums stay in its registers
 // until the block's last row and leave as one row of partial sums.
 template <int EB, int NT, int UPT, int R, bool RAGGED>

@@ -18,6 +18,12 @@
 // every kernel that moves rows walks tokens, so that a token's row is read (or
 // written) once and each sorted row is touched by exactly one token.  dest is
 // checked against the rows' bounds before it is used as an address.
+//
+// MI355X: dispatch of 16384 x 8 rows of 2048 bf16 114 us (5.3 TB/s; a copy of as
+// many bytes 94), 13 us of it the sort's two launches; both gradients of 8192 x
+// 8 rows of 4096 bf16 330 us (5.3 TB/s; 270); combine of 4099 x 6 rows of 1000
+// fp32 17.2 us (6.7 TB/s, partly from the last-level cache; 17.8); dispatch of 4
+// tokens 6.3 us in one launch, the kernel 3.9.
 #include "ops.h"
 #include "ops_device.h"
 
