@@ -474,10 +474,7 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
     size_t r = blockIdx.x;
     int my_at = -1;                 // this thread's entry of the row
     float my_t = -INFINITY, my_z = 0.0f;
-    if (tid < top) {
-        my_at = entry(r, tid, &my_t);
-        if (my_at >= 0) my_z = logit(r, my_at);
-    }
+    if (tid < top) my_at = entry(r, tid, &my_t);
     {
         const char* z = static_cast<const char*>(a.logits) + r * a.lstride * EB;
 #pragma unroll
@@ -486,6 +483,7 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
             if (live(u)) raw[u] = ld_unit<EB, true>(z + place(u).at * EB);
         }
     }
+    if (my_at >= 0) my_z = logit(r, my_at);   // (the row's loads are on their way)
     const auto stage = [&](int b) {
         if (tid < top) {
             my_t = my_at >= 0 ? my_t : -INFINITY;
