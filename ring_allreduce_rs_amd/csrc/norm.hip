@@ -216,14 +216,16 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_grad_narrow(const NormGra
     put_columns<E>(a, at, dw, db);
 }
 
-// Rows that a block holds in registers: NT threads with UPT units each, R rows
-// at a time, so that a block has R rows of loads in flight and one barrier
+// Rows that a block holds in registers: up to NT threads (FIXED: exactly) with
+// UPT units each, R
+// rows at a time, so that a block has R rows of loads in flight and one barrier
 // serves R sums.  The parameters stay in registers from row to row.  Rows past
 // the last are loaded as the last one again and left out of sums and stores.
-template <int EB, int NT, int UPT, int R, bool RAGGED>
+template <int EB, int NT, int UPT, int R, bool RAGGED, bool FIXED>
 __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
-    constexpr int E = Vec<EB>::E, W = NT / 64;
-    __shared__ float lds[2][W * R];
+    constexpr int E = Vec<EB>::E;
+    __shared__ float lds[2][NT / 64 * R];
+    const int nt = FIXED ? NT : (int)blockDim.x, waves = nt >> 6;
     const float n = (float)a.cols;
     Place at[UPT];
     u32x4 raw[R][UPT];
@@ -239,7 +241,7 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
     };
 #pragma unroll
     for (int u = 0; u < UPT; ++u)
-        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
+        at[u] = place_unit<E>((u * nt + threadIdx.x) * E, (unsigned)a.cols);
     size_t r0 = (size_t)blockIdx.x * R;
     load(r0);   // (ahead of the parameters: one round trip for both)
     float w[UPT][E], b[UPT][E];
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
                 for (int j = 0; j < E; ++j) mean[k] += v[j];
             }
         }
-        block_sums<W, R>(mean, lds[0]);
+        block_sums<R>(mean, lds[0], waves);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mean[k] /= n;
@@ -284,7 +286,7 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
                 }
             }
         }
-        block_sums<W, R>(s, lds[1]);
+        block_sums<R>(s, lds[1], waves);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             if (r0 + k >= a.rows) break;
@@ -312,10 +314,11 @@ __global__ __launch_bounds__(NT) void k_norm_rows(const NormArgs a) {
 // took 164 us in all at 8192 x 8192 bf16, this form 79.6).  Each thread owns the same columns
 // in every row that its block takes, so the column sums stay in its registers
 // until the block's last row and leave as one row of partial sums.
-template <int EB, int NT, int UPT, int R, bool RAGGED>
+template <int EB, int NT, int UPT, int R, bool RAGGED, bool FIXED>
 __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
-    constexpr int E = Vec<EB>::E, W = NT / 64;
-    __shared__ float lds[2][W * 2 * R];
+    constexpr int E = Vec<EB>::E;
+    __shared__ float lds[2][NT / 64 * 2 * R];
+    const int nt = FIXED ? NT : (int)blockDim.x, waves = nt >> 6;
     const float inv = 1.0f / (float)a.cols;
     Place at[UPT];
     u32x4 rx[R][UPT], rg[R][UPT];
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
     };
 #pragma unroll
     for (int u = 0; u < UPT; ++u)
-        at[u] = place_unit<E>((u * NT + threadIdx.x) * E, (unsigned)a.cols);
+        at[u] = place_unit<E>((u * nt + threadIdx.x) * E, (unsigned)a.cols);
     size_t r0 = (size_t)blockIdx.x * R;
 #pragma unroll
     for (int k = 0; k < R; ++k) load(r0, k);
@@ -385,7 +388,7 @@ __global__ __launch_bounds__(NT) void k_norm_grad_rows(const NormGradArgs a) {
                 }
             __builtin_amdgcn_sched_barrier(0);   // one row's temporaries at a time
         }
-        block_sums<W, 2 * R>(s, lds[buf]);
+        block_sums<2 * R>(s, lds[buf], waves);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const float c1 = s[2 * k] * inv, c2 = s[2 * k + 1] * inv;
@@ -583,6 +586,8 @@ static unsigned row_blocks(size_t rows) {
 struct RowShape {
     int threads, upt, r;
 };
+// A block has the wavefronts that a row's units need: 8192 x 5120 bf16 forwards
+// takes 46 us with 640 threads and 57 with 1024.
 static RowShape row_shape(size_t cols, int eb) {
     if (cols < 16u / eb) return {0, 0, 0};   // no 16 bytes in a row
     const size_t units = (cols * eb + 15) / 16;
@@ -590,12 +595,12 @@ static RowShape row_shape(size_t cols, int eb) {
         const int tpr = units <= 8 ? 8 : units <= 16 ? 16 : 32;
         return {tpr, 1, kNormWaves * kNarrowSteps * 64 / tpr};
     }
-    if (units <= 64) return {64, 1, 4};
-    if (units <= 256) return {256, 1, 4};
-    if (units <= 512) return {512, 1, 4};
-    if (units <= 1024) return {1024, 1, 4};
-    if (units <= 2048) return {1024, 2, 1};
-    if (units <= 4096 && eb == 4) return {1024, 4, 1};
+    const auto threads = [&](size_t upt) {
+        return (int)((units + 64 * upt - 1) / (64 * upt) * 64);
+    };
+    if (units <= 1024) return {threads(1), 1, 4};
+    if (units <= 2048) return {threads(2), 2, 1};
+    if (units <= 4096 && eb == 4) return {threads(4), 4, 1};
     return {0, 0, 0};
 }
 
@@ -609,7 +614,8 @@ static RowShape row_shape(size_t cols, int eb) {
 static size_t grad_blocks(size_t rows, size_t cols, RowShape sh) {
     const size_t steps = (rows + sh.r - 1) / sh.r;
     if (steps <= 2) return rows ? 1 : 0;
-    const size_t most = sh.threads < 64 ? 1024 : 4096 / (sh.threads / 64);
+    // (whole rounds of the compute units: 16 wavefronts each, blocks not divided)
+    const size_t most = sh.threads < 64 ? 1024 : kCUs * (1024 / sh.threads);
     const double c = cols * 2e-6 > 0.00625 ? cols * 2e-6 : 0.00625;
     const size_t best = (size_t)std::sqrt(3.0 * (double)steps / c) + 1;
     const size_t p = best < most ? best : most;
@@ -623,15 +629,15 @@ size_t norm_grad_parts(size_t rows, size_t cols, int eb) {
     return p < kColParts ? p : kColParts;
 }
 
-#define ROWS_BY_SHAPE(EB, RAGGED, CALL)                                       \
-    switch (sh.threads * 8 + sh.upt) {                                        \
-        case 64 * 8 + 1: { CALL(EB, 64, 1, 4, RAGGED); } break; \
-        case 256 * 8 + 1: { CALL(EB, 256, 1, 4, RAGGED); } break; \
-        case 512 * 8 + 1: { CALL(EB, 512, 1, 4, RAGGED); } break; \
-        case 1024 * 8 + 1: { CALL(EB, 1024, 1, 4, RAGGED); } break; \
-        case 1024 * 8 + 2: { CALL(EB, 1024, 2, 1, RAGGED); } break; \
-        default: if constexpr (EB == 4) { CALL(EB, 1024, 4, 1, RAGGED); } break; \
-    }
+#define ROWS_BY_SHAPE(EB, RAGGED, CALL)                             \
+    if (sh.upt == 2) { CALL(EB, 1024, 2, 1, RAGGED); }              \
+    else if (sh.upt == 4) {                                         \
+        if constexpr (EB == 4) { CALL(EB, 1024, 4, 1, RAGGED); }    \
+    }                                                               \
+    else if (sh.threads <= 64) { CALL(EB, 64, 1, 4, RAGGED); }      \
+    else if (sh.threads <= 256) { CALL(EB, 256, 1, 4, RAGGED); }    \
+    else if (sh.threads <= 512) { CALL(EB, 512, 1, 4, RAGGED); }    \
+    else { CALL(EB, 1024, 1, 4, RAGGED); }
 #define NARROW_BY_SHAPE(EB, RAGGED, CALL)                   \
     if (sh.threads == 8) { CALL(EB, 8, RAGGED); }           \
     else if (sh.threads == 16) { CALL(EB, 16, RAGGED); }    \
@@ -663,13 +669,18 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
         return hipGetLastError();
     }
     // one row a block until every compute unit has rows at R a block
+    const dim3 block(sh.threads);
     const bool few = a.rows <= (size_t)kCUs * sh.r;
     if (few) grid.x = (unsigned)a.rows;
-#define CALL(EB, NT, UPT, R, RAGGED)                                                             \
-    if (few) hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, 1, RAGGED>), grid, dim3(NT), 0, s, a); \
-    else hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, R, RAGGED>), grid, dim3(NT), 0, s, a)
+#define LAUNCH(EB, NT, UPT, R, RAGGED, FIXED) \
+    hipLaunchKernelGGL((k_norm_rows<EB, NT, UPT, R, RAGGED, FIXED>), grid, block, 0, s, a)
+#define CALL(EB, NT, UPT, R, RAGGED)                                          \
+    if (few) LAUNCH(EB, NT, UPT, 1, RAGGED, false);                           \
+    else if (sh.threads == NT && !RAGGED) LAUNCH(EB, NT, UPT, R, RAGGED, !RAGGED); \
+    else LAUNCH(EB, NT, UPT, R, RAGGED, false)
     BY_TYPE(ROWS_BY_SHAPE, CALL)
 #undef CALL
+#undef LAUNCH
     return hipGetLastError();
 }
 
@@ -691,17 +702,21 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
     const size_t parts = norm_grad_parts(a.rows, a.cols, a.eb);
     const RowShape sh = row_shape(a.cols, a.eb);
     if (a.rows > 0 && sh.threads) {
-        const dim3 grid((unsigned)parts);
+        const dim3 grid((unsigned)parts), block(sh.threads);
         if (sh.threads < 64) {
 #define CALL(EB, TPR, RAGGED) \
     hipLaunchKernelGGL((k_norm_grad_narrow<EB, TPR, RAGGED>), grid, dim3(kNormThreads), 0, s, a)
             BY_TYPE(NARROW_BY_SHAPE, CALL)
 #undef CALL
         } else {
-#define CALL(EB, NT, UPT, R, RAGGED) \
-    hipLaunchKernelGGL((k_norm_grad_rows<EB, NT, UPT, R, RAGGED>), grid, dim3(NT), 0, s, a)
+#define LAUNCH(EB, NT, UPT, R, RAGGED, FIXED) \
+    hipLaunchKernelGGL((k_norm_grad_rows<EB, NT, UPT, R, RAGGED, FIXED>), grid, block, 0, s, a)
+#define CALL(EB, NT, UPT, R, RAGGED)                                                   \
+    if (sh.threads == NT && !RAGGED) LAUNCH(EB, NT, UPT, R, RAGGED, !RAGGED);          \
+    else LAUNCH(EB, NT, UPT, R, RAGGED, false)
             BY_TYPE(ROWS_BY_SHAPE, CALL)
 #undef CALL
+#undef LAUNCH
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || parts == 1) return e;

@@ -330,32 +330,31 @@ __device__ __forceinline__ float block_sum(float v, float* lds) {
     return t;
 }
 
-// V sums over a block of W wavefronts at once (V a power of two), on every
-// thread.  `lds` holds W * V floats; the barrier inside is the only one, so a
-// caller that comes back before another barrier takes another buffer.
-template <int W, int V>
-__device__ __forceinline__ void block_sums(float (&v)[V], float* lds) {
+// V sums over a block's `waves` wavefronts at once (V a power of two), on every
+// thread.  `lds` holds V floats a wavefront; the barrier inside is the only
+// one, so a caller that comes back before another barrier takes another buffer.
+template <int V>
+__device__ __forceinline__ void block_sums(float (&v)[V], float* lds, int waves) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = wave_sum(v[i]);
-    if constexpr (W > 1) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        float mine = v[0];
+    if (waves == 1) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float mine = v[0];
 #pragma unroll
-        for (int i = 1; i < V; ++i) mine = lane == i ? v[i] : mine;
-        if (lane < V) lds[wave * V + lane] = mine;
-        __syncthreads();
-        // lane l takes sum l % V of every (64 / V)th wavefront
-        float t = 0.0f;
+    for (int i = 1; i < V; ++i) mine = lane == i ? v[i] : mine;
+    if (lane < V) lds[wave * V + lane] = mine;
+    __syncthreads();
+    // lane l takes sum l % V of every (64 / V)th wavefront
+    float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; w += 64 / V)
-            if (w + lane / V < W) t += lds[w * V + lane];
+    for (int w = 0; w < 16; w += 64 / V)
+        if (w + lane / V < waves) t += lds[w * V + lane];
 #pragma unroll
-        for (int d = V; d < 64; d <<= 1)
-            if (d / V < W) t += __shfl_xor(t, d, 64);
+    for (int d = V; d < 64; d <<= 1)
+        if (d / V < 16) t += __shfl_xor(t, d, 64);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            v[i] = as_f32((uint32_t)__builtin_amdgcn_readlane((int)as_u32(t), i));
-    }
+    for (int i = 0; i < V; ++i)
+        v[i] = as_f32((uint32_t)__builtin_amdgcn_readlane((int)as_u32(t), i));
 }
 
 }  // namespace arlib

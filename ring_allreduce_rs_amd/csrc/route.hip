@@ -425,7 +425,7 @@ __global__ __launch_bounds__(NT) void k_route_combine_grad(const CombineArgs a) 
                     IO::st(static_cast<char*>(a.drows) + (size_t)d * a.hidden * EB, p, hidden, out);
                 }
             }
-            block_sums<W, KB>(dot, lds[buf]);
+            block_sums<KB>(dot, lds[buf], W);
 #pragma unroll
             for (int k = 0; k < KB; ++k)
                 if (threadIdx.x == 0 && k0 + k < a.topk) {
