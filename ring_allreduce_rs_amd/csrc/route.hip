@@ -21,7 +21,7 @@
 //
 // MI355X: dispatch of 16384 x 8 rows of 2048 bf16 114 us (5.3 TB/s; a copy of as
 // many bytes 94), 13 us of it the sort's two launches; both gradients of 8192 x
-// 8 rows of 4096 bf16 330 us (5.3 TB/s; 270); combine of 4099 x 6 rows of 1000
+// 8 rows of 4096 bf16 314 us (5.6 TB/s; 270); combine of 4099 x 6 rows of 1000
 // fp32 17.2 us (6.7 TB/s, partly from the last-level cache; 17.8); dispatch of 4
 // tokens 6.3 us in one launch, the kernel 3.9.
 #include "ops.h"
@@ -393,7 +393,8 @@ __global__ __launch_bounds__(NT) void k_route_combine_grad(const CombineArgs a) 
             for (int k = 0; k < KB; ++k) dot[k] = 0.0f;
             for (unsigned i = threadIdx.x; i < units; i += NT) {
                 const Place p = IO::place(i, hidden);
-                u32x4 raw[KB], rg = IO::ld(dy, p, hidden);
+                // (the token's gradient was written just now, the rows were not)
+                u32x4 raw[KB], rg = RowIO<EB, MODE, false>::ld(dy, p, hidden);
 #pragma unroll
                 for (int k = 0; k < KB; ++k) {
                     const int d = k0 + k < a.topk ? ld_uniform(a.dest + t * a.topk + k0 + k) : -1;
@@ -443,12 +444,13 @@ unsigned token_blocks(int tokens) {
     return (unsigned)(tokens < kMost ? tokens : kMost);
 }
 
-// Threads of a token's block: a row's units, at most 256, or 1024 while there
-// are fewer tokens than compute units (both gradients of 56 x 4 rows of 5742
-// fp32 11.7 us against 19.3 with 256).
+// Threads of a token's block: a row's units, at most 512, or 1024 while there
+// are fewer tokens than compute units (both gradients of 8192 x 8 rows of 4096
+// bf16 323 us with 512 threads, 329 with 256; of 56 x 4 rows of 5742 fp32 11.7 us
+// with 1024, 19.3 with 256).
 int token_threads(size_t tokens, size_t hidden, int eb) {
     const size_t units = (hidden * eb + 15) / 16;
-    return units <= 64 ? 64 : units <= 128 ? 128 : units <= 256 || tokens > 256 ? 256 : 1024;
+    return units <= 64 ? 64 : units <= 128 ? 128 : units <= 256 ? 256 : tokens > 256 ? 512 : 1024;
 }
 
 // The direct form's comparisons: every token with every slot, 8 choices at a
@@ -492,6 +494,7 @@ int sort_blocks(size_t slots) {
         if (nt == 64) BY_MODE(EB, 64, CALL); \
         else if (nt == 128) BY_MODE(EB, 128, CALL); \
         else if (nt == 256) BY_MODE(EB, 256, CALL); \
+        else if (nt == 512) BY_MODE(EB, 512, CALL); \
         else BY_MODE(EB, 1024, CALL);       \
     } while (0)
 #define BY_ROW(CALL)                                        \
@@ -507,9 +510,9 @@ int sort_blocks(size_t slots) {
     do {                                                                        \
         const int nt = token_threads((size_t)a.tokens, a.hidden, a.eb);         \
         const RowMode mode = row_mode(a.hidden, a.eb);                          \
-        if (a.eb == 2 && nt <= 256) BY_MODE(2, 256, CALL);                      \
+        if (a.eb == 2 && nt <= 512) BY_MODE(2, 256, CALL);                      \
         else if (a.eb == 2) BY_MODE(2, 1024, CALL);                             \
-        else if (nt <= 256) BY_MODE(4, 256, CALL);                              \
+        else if (nt <= 512) BY_MODE(4, 256, CALL);                              \
         else BY_MODE(4, 1024, CALL);                                            \
     } while (0)
 
