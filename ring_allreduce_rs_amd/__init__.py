@@ -11,6 +11,10 @@ CPU fallback: if libar.so is missing, importing this package raises.
 The API mirrors ``torch.distributed.all_reduce`` semantics ("Allreduce：大模型
 分布式训练的核心通信算法与优化实践", section 3.2: in place, every participant
 ends with the same reduced tensor), with the participants given as a list.
+
+Beside the collectives stand the operators that a training step runs between
+two AllReduces: ``layer_norm``, ``expert_dispatch`` / ``expert_combine`` and
+``distill_loss`` / ``distill_step`` with their gradients (operators.py).
 """
 
 from __future__ import annotations
@@ -19,8 +23,8 @@ import ctypes
 
 from . import _lib
 from ._lib import (  # noqa: F401
-    ALGOS, AR_GRAPHS_MAX_BYTES_DEFAULT, AR_MAX_RANKS, DTYPES, EXPORTS, LIB_PATH, OPS, ArError,
-    Context, auto_algo, chunk_range, lib, predict_us,
+    ALGOS, AR_DISTILL_MAX_TOP, AR_GRAPHS_MAX_BYTES_DEFAULT, AR_MAX_EXPERTS, AR_MAX_RANKS, DTYPES,
+    EXPORTS, LIB_PATH, OPS, ArError, Context, auto_algo, chunk_range, lib, predict_us,
 )
 
 __all__ = [
