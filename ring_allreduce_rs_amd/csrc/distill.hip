@@ -15,7 +15,7 @@
 //
 // MI355X: step of 4096 x 131072 bf16 408 us (5.3 TB/s; a copy of as many bytes
 // 332), where two passes over the logits took 556; gradient of 2047 x 50021 fp32
-// 155 us (5.3 TB/s; 127); loss of 1 x 131072 fp32 in two launches 7-8 us and
+// 155 us (5.3 TB/s; 127); loss of 1 x 131072 fp32 in two launches 7-9 us and
 // step of 8 x 32000 bf16 7.9 us, both bound by launches and round trips.  A
 // step's exponentials, two a logit at a quarter of the vector rate, take about
 // 60 % of the time that its bytes take, which is why they have to overlap.
