@@ -574,9 +574,10 @@ __global__ __launch_bounds__(kFoldThreads) void k_norm_fold(const NormGradArgs a
 
 }  // namespace
 
-// Rows of a launch: the kernels walk the rest (a grid holds fewer than 2^32 threads).
+// Rows of a launch: the kernels walk the rest (a grid holds fewer than 2^32
+// threads, a block up to 2^10 of them).
 static unsigned row_blocks(size_t rows) {
-    constexpr size_t kMost = size_t(1) << 22;
+    constexpr size_t kMost = size_t(1) << 21;
     return (unsigned)(rows < kMost ? rows : kMost);
 }
 

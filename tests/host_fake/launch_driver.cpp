@@ -1,0 +1,142 @@
+// launch_driver.cpp -- runs the training operators' launchers (norm.hip,
+// route.hip, distill.hip, host side only) against a HIP runtime that records
+// each launch instead of running it.  Test infrastructure only: prints "ALL OK"
+// and exits 0 when every check of the section named on the command line passes.
+//
+// Every launch of every section has to be one that HIP accepts: blocks of
+// 1 .. 1024 threads, fewer than 2^32 threads in each dimension of the grid.
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+#include <map>
+#include <string>
+#include <vector>
+
+#include "ops.h"
+
+namespace {
+
+struct Launch {
+    std::string kernel;   // mangled
+    dim3 grid, block;
+    size_t lds;
+};
+// kernels by their host address (the objects register them before main, in any order)
+std::map<const void*, std::string>& names() {
+    static std::map<const void*, std::string> m;
+    return m;
+}
+std::vector<Launch> g_launches;
+Launch g_call;
+int g_fail = 0;
+
+#define CHECK(c)                                                              \
+    do {                                                                      \
+        if (!(c)) {                                                           \
+            std::fprintf(stderr, "FAIL %s:%d: %s\n", __FILE__, __LINE__, #c); \
+            ++g_fail;                                                         \
+        }                                                                     \
+    } while (0)
+
+}  // namespace
+
+extern "C" {
+hipError_t hipGetLastError() { return hipSuccess; }
+hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t lds, hipStream_t) {
+    g_call = Launch{"", grid, block, lds};
+    return hipSuccess;
+}
+hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipStream_t* s) {
+    *grid = g_call.grid;
+    *block = g_call.block;
+    *lds = g_call.lds;
+    *s = nullptr;
+    return hipSuccess;
+}
+hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void**, size_t lds, hipStream_t) {
+    g_launches.push_back({names()[f], grid, block, lds});
+    return hipSuccess;
+}
+void** __hipRegisterFatBinary(const void*) {
+    static void* handle;
+    return &handle;
+}
+void __hipRegisterFunction(void**, const void* host, char*, const char* name, unsigned, void*, void*,
+                           void*, void*, int*) {
+    names()[host] = name;
+}
+void __hipUnregisterFatBinary(void**) {}
+}
+
+namespace {
+
+// What `call` launches, each of them one that HIP accepts.
+template <class F>
+std::vector<Launch> launches(const char* what, F call) {
+    g_launches.clear();
+    CHECK(call() == hipSuccess);
+    for (const Launch& l : g_launches) {
+        const uint64_t g[3] = {l.grid.x, l.grid.y, l.grid.z}, b[3] = {l.block.x, l.block.y, l.block.z};
+        bool good = b[0] * b[1] * b[2] >= 1 && b[0] * b[1] * b[2] <= 1024;
+        for (int i = 0; i < 3; ++i)
+            good = good && g[i] >= 1 && g[i] * b[i] < (uint64_t(1) << 32);
+        if (!good) {
+            std::fprintf(stderr, "FAIL %s: %s, grid (%u, %u, %u) of (%u, %u, %u) threads\n", what,
+                         l.kernel.c_str(), l.grid.x, l.grid.y, l.grid.z, l.block.x, l.block.y,
+                         l.block.z);
+            ++g_fail;
+        }
+    }
+    return g_launches;
+}
+
+// Not dereferenced: a launcher only passes arrays on.
+template <class T = void>
+T* array() {
+    return reinterpret_cast<T*>(uintptr_t(1) << 44);
+}
+
+arlib::NormArgs norm(size_t rows, size_t cols, int eb) {
+    return {array(), array(), array(), array(), array<float>(), array<float>(), cols, rows, cols,
+            1e-5f,   eb,      4};
+}
+
+arlib::NormGradArgs norm_grad(size_t rows, size_t cols, int eb, bool columns = true) {
+    return {array(), array(), array<float>(), array<float>(), array(), array(),
+            columns ? array() : nullptr, columns ? array() : nullptr, array<float>(), cols, cols,
+            rows, cols, eb, 4};
+}
+
+// More rows than a grid's blocks: the kernels walk the rest.
+void rows() {
+    for (const int eb : {2, 4})
+        for (const size_t cols : {1, 5, 64, 200, 771, 1024, 4096, 5001, 8192, 16384, 20000})
+            for (const size_t n : {size_t(1), size_t(255), size_t(1) << 22, (size_t(1) << 24) + 5,
+                                   (size_t(1) << 33) + 1}) {
+                launches("norm", [&] { return arlib::launch_norm(norm(n, cols, eb), nullptr); });
+                launches("norm gradient",
+                         [&] { return arlib::launch_norm_grad(norm_grad(n, cols, eb), nullptr); });
+            }
+}
+
+struct Section {
+    const char* name;
+    void (*run)();
+};
+const Section kSections[] = {{"rows", rows}};
+
+}  // namespace
+
+int main(int argc, char** argv) {
+    for (const Section& s : kSections)
+        if (argc == 2 && !std::strcmp(argv[1], s.name)) {
+            s.run();
+            if (g_fail) return 1;
+            std::printf("ALL OK\n");
+            return 0;
+        }
+    std::fprintf(stderr, "no such section\n");
+    return 2;
+}
