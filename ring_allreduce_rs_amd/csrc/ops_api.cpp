@@ -24,7 +24,7 @@ size_t float_bytes(int dtype) {
 }
 
 // Widest row of a layer norm, of the experts and of the logits (byte offsets within a row stay
-// below 2^32, and so do the column sums' threads).
+// below 2^32).
 constexpr size_t kMostCols = size_t(1) << 28;
 
 // *out = a * b, false on overflow.

@@ -121,11 +121,23 @@ void rows() {
             }
 }
 
+// Rows up to the widest that the operators take.
+void widths() {
+    for (const int eb : {2, 4})
+        for (const size_t cols : {(size_t(1) << 27) - 1, size_t(1) << 27, (size_t(1) << 28) - 3,
+                                  size_t(1) << 28})
+            for (const size_t n : {size_t(1), size_t(70), size_t(100000)}) {
+                launches("norm", [&] { return arlib::launch_norm(norm(n, cols, eb), nullptr); });
+                launches("norm gradient",
+                         [&] { return arlib::launch_norm_grad(norm_grad(n, cols, eb), nullptr); });
+            }
+}
+
 struct Section {
     const char* name;
     void (*run)();
 };
-const Section kSections[] = {{"rows", rows}};
+const Section kSections[] = {{"rows", rows}, {"widths", widths}};
 
 }  // namespace
 

@@ -48,3 +48,7 @@ def driver(tmp_path_factory):
 
 def test_more_rows_than_blocks(driver):
     driver("rows")
+
+
+def test_the_widest_rows(driver):
+    driver("widths")
