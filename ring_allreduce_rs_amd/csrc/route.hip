@@ -403,7 +403,12 @@ __global__ __launch_bounds__(NT) void k_route_combine_grad(const CombineArgs a) 
                         raw[k] = IO::ld(static_cast<const char*>(a.rows) +
                                             (size_t)d * a.hidden * EB, p, hidden);
                 }
-                if (MODE == ROW_RAGGED && p.skip) rg = drop_first<EB, true>(rg, p.skip);
+                if (MODE == ROW_RAGGED && p.skip) {
+                    rg = drop_first<EB, true>(rg, p.skip);
+                    // (an infinity there would make NaN of the dropped 0)
+#pragma unroll
+                    for (int k = 0; k < KB; ++k) raw[k] = drop_first<EB, true>(raw[k], p.skip);
+                }
                 float g[E];
                 Vec<EB>::unpack(rg, g);
 #pragma unroll
