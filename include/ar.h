@@ -526,6 +526,8 @@ ar_status ar_expert_combine_backward(ar_ctx* ctx, const void* dy, size_t dy_stri
  *   loss = T^2 * sum over entries of p * (log p - log q at their places)
  * An entry with p == 0 adds nothing; a place named twice counts twice; a row
  * that keeps no entry (or whose kept teacher logits are all -inf) has loss 0.
+ * A kept teacher logit that is +inf or NaN makes its row's p, and so the loss
+ * and the gradient at the entries' places, NaN.
  * loss and lse: binary32, rows.  teacher has the logits' dtype.  Limits
  * (AR_ERR_UNSUPPORTED): top <= AR_DISTILL_MAX_TOP, vocab <= 2^28.
  * vocab and top > 0; rows == 0 is a successful no-op. */

@@ -7,7 +7,8 @@
 //   loss = T^2 sum_j p_j (log p_j - log q_{i_j})
 //   d loss / d z_v = T (q_v - sum_{j: i_j = v} p_j)
 // An entry with p_j = 0 adds nothing.  A row without a kept entry (or whose
-// teacher logits are all -inf) has loss 0 and gradient 0, whatever z holds.
+// teacher logits are all -inf) has loss 0 and gradient 0, whatever z holds; a
+// kept +inf or NaN among the teacher's makes every p_j of its row NaN.
 //
 // All sums are fp32 and are split the same way at every call, so results
 // repeat bit for bit.  The traffic is the logits and their gradient; the
@@ -88,7 +89,8 @@ __device__ __forceinline__ float block_max(float v, float* lds) {
 }
 
 // Fills th for row r; returns whether the row has a teacher.  *zmax and *logs
-// are what log p_j = t_j / T - zmax - logs takes.  All threads call it.
+// are what log p_j = t_j / T - zmax - logs takes.  A +inf logit less itself
+// makes the sum, and so every p_j, NaN.  All threads call it.
 template <int EB, int IB, int W>
 __device__ bool load_teacher(const DistillArgs& a, size_t r, Teacher& th, float* zmax,
                              float* logs) {
@@ -553,6 +555,7 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
         if constexpr (kSums)
             zs = wave_soft({has ? red[b].m[w] : -INFINITY, has ? red[b].s[w] : 0.0f}, c);
         ts = wave_soft({has ? red[b].tm[w] : -INFINITY, has ? red[b].ts[w] : 0.0f}, c);
+        if (ts.m == INFINITY) ts.s = NAN;   // (no softmax, as in load_teacher)
         const bool some = !(ts.s == 0.0f);
         const float scale = kGrad ? a.dloss[r] * a.temperature : 0.0f;
         const float base = soft_base(zs.m), logz = logf(zs.s), inv = 1.0f / zs.s;

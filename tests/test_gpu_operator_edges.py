@@ -50,3 +50,46 @@ def test_infinite_rows_beside_a_ragged_end(hidden, t):
         assert int(torch.isinf(dw).sum()) == 2
         ref.close(got[0], drows, tdrows, "drows")
         ref.close(got[1], dw, torch.where(torch.isinf(dw), 0.0, tdw), "dweights")
+
+
+# (rows, vocab): rows in registers, more of them than blocks, chunks of one row, a row's
+# parts, chunks of a block's row
+FORMS = [(6, 300), (6, 32000), (700, 4099), (7000, 1003), (3, 140001), (600, 140001), (3, 5)]
+
+
+def distill_case(rows, vocab, top, t, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    logits = (torch.randn((rows, vocab), generator=g, device="cuda") * 2.5).to(t)
+    at = torch.randint(0, vocab, (rows, top), generator=g, device="cuda")
+    teacher = (torch.randn((rows, top), generator=g, device="cuda") * 2 + 4).to(t)
+    return logits, at, teacher, torch.rand(rows, generator=g, device="cuda") + 0.5
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_infinite_teacher_logits(rows, vocab, t):
+    """A kept +inf has no softmax: the row's loss and its gradient at the entries'
+    places are NaN, in every form; left out, it is not looked at."""
+    logits, at, teacher, dloss = distill_case(rows, vocab, 4, t, 11)
+    bad = torch.tensor([1, rows - 1], device="cuda")
+    clean, lse = ar.distill_loss(logits, at, teacher)
+    clean_step = ar.distill_step(dloss, logits, at, teacher)
+    clean_back = ar.distill_backward(dloss, logits, at, teacher, lse)
+    teacher[bad, 2] = float("inf")
+    at[0, 1] = -1
+    teacher[0, 1] = float("inf")
+    loss, got = ar.distill_loss(logits, at, teacher)
+    step = ar.distill_step(dloss, logits, at, teacher)
+    back = ar.distill_backward(dloss, logits, at, teacher, lse)
+    assert torch.equal(got, lse)
+    named = torch.zeros((rows, vocab), dtype=torch.bool, device="cuda")
+    named.scatter_(1, at.clamp(min=0), True)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    for v, c in ((loss, clean), (step[0], clean_step[0])):
+        assert torch.isnan(v[bad]).all() and torch.isfinite(v[0])
+        assert torch.equal(v[1:][keep[1:]], c[1:][keep[1:]])
+    for v, c in ((step[1], clean_step[1]), (back, clean_back)):
+        assert torch.isnan(v[bad][named[bad]]).all()
+        assert torch.equal(v[bad][~named[bad]], c[bad][~named[bad]])
+        assert torch.equal(v[1:][keep[1:]], c[1:][keep[1:]]) and torch.isfinite(v[0]).all()
