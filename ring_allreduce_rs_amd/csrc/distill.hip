@@ -150,6 +150,10 @@ __device__ __forceinline__ Soft soft_zero() { return {-INFINITY, 0.0f}; }
 // What the sum is relative to: an infinite maximum is left out, so that a row
 // of -inf sums to 0 and a +inf makes the sum (and lse) infinite.
 __device__ __forceinline__ float soft_base(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
+// What q's exponentials are relative to: a +inf maximum, whose sum is infinite,
+// stays, so that every finite value has exp(-inf) = 0 however large it is, and
+// the infinite one NaN.
+__device__ __forceinline__ float soft_top(float m) { return m > -INFINITY ? m : 0.0f; }
 // The base that a sum of this maximum has, seen from another: -inf for an
 // empty one, so that its 0 stays 0.
 __device__ __forceinline__ float soft_from(float m) { return m < INFINITY ? m : 0.0f; }
@@ -370,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
         float base = 0.0f, lse = 0.0f, inv = 1.0f;
         if constexpr (PARTS) {
             const Soft v = fold_parts(a, r, soft_parts, c);
-            base = soft_base(v.m);
+            base = soft_top(v.m);
             inv = 1.0f / v.s;
             if (lo == 0) {   // (uniform over the block)
                 const float loss =
@@ -558,7 +562,7 @@ __global__ __launch_bounds__(1024) void k_distill_rows(const DistillArgs a) {
         if (ts.m == INFINITY) ts.s = NAN;   // (no softmax, as in load_teacher)
         const bool some = !(ts.s == 0.0f);
         const float scale = kGrad ? a.dloss[r] * a.temperature : 0.0f;
-        const float base = soft_base(zs.m), logz = logf(zs.s), inv = 1.0f / zs.s;
+        const float base = soft_top(zs.m), logz = logf(zs.s), inv = 1.0f / zs.s;
         const float lse = kSums ? 0.0f : a.lse_in[r];
         const float tbase = soft_base(ts.m), logs = logf(ts.s), tinv = 1.0f / ts.s;
         char* dz = static_cast<char*>(a.dlogits) + r * a.vocab * EB;

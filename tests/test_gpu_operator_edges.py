@@ -93,3 +93,29 @@ def test_infinite_teacher_logits(rows, vocab, t):
         assert torch.isnan(v[bad][named[bad]]).all()
         assert torch.equal(v[bad][~named[bad]], c[bad][~named[bad]])
         assert torch.equal(v[1:][keep[1:]], c[1:][keep[1:]]) and torch.isfinite(v[0]).all()
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_large_logits_beside_an_infinite_one(rows, vocab, t):
+    """A +inf makes the row's sum infinite: q is 0 at every finite logit, however
+    large, and NaN at the infinite one, by the step as by loss and backward."""
+    logits, at, teacher, dloss = distill_case(rows, vocab, 2, t, 12)
+    bad = torch.tensor([1, rows - 1], device="cuda")
+    logits[bad, vocab // 2] = float("inf")
+    logits[bad, 0] = 200.0        # exp(200) is past fp32
+    logits[bad, vocab - 1] = torch.finfo(t).max
+    at[bad] = torch.tensor([0, 1], device="cuda")
+    loss, lse = ar.distill_loss(logits, at, teacher)
+    step = ar.distill_step(dloss, logits, at, teacher)
+    back = ar.distill_backward(dloss, logits, at, teacher, lse)
+    assert (loss[bad] == float("inf")).all() and (lse[bad] == float("inf")).all()
+    assert (step[0][bad] == float("inf")).all()
+    p = teacher.double().softmax(1)[bad] * dloss.double()[bad, None]
+    # two exponentials, their sum, a quotient and a product, then the last rounding
+    tol = p * (2 * ref.EXP + 8 * ref.U + ref.half_step(t))
+    for d in (step[1][bad], back[bad]):
+        assert torch.isnan(d[:, vocab // 2]).all()
+        ref.close(d[:, :2], -p, tol)
+        rest = torch.cat([d[:, 2:vocab // 2], d[:, vocab // 2 + 1:]], 1)
+        assert not rest.any()
