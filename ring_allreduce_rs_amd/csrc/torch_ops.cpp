@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -70,9 +71,18 @@ std::string shape_of(const at::Tensor& t) {
     return s + ")";
 }
 
+// A tensor argument.  The outputs have no history, so one whose gradient (or
+// forward-mode tangent) would be lost is refused.
 const at::Tensor& tensor(PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) throw Refused(std::string(name) + " is not a tensor");
-    return THPVariable_Unpack(o);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        throw Refused(std::string(name) + " requires grad, which this call does not record: "
+                      "detach it or call under torch.no_grad()");
+    if (t._fw_grad(0).defined())
+        throw Refused(std::string(name) + " has a forward-mode tangent, which this call does not "
+                      "carry on");
+    return t;
 }
 
 ar_dtype dtype_of(const at::Tensor& t, const char* name) {

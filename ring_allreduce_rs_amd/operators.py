@@ -8,7 +8,9 @@ outputs (and scratch, where an operator needs some) from torch's allocator, and
 enqueues the HIP kernels of libar.so on torch's current stream (include/ar.h
 holds the formulas and limits; csrc/torch_ops.cpp is the binding).  Nothing is
 recorded for torch's autograd: the gradients are the ``*_backward`` functions
-(and ``distill_step``).
+(and ``distill_step``).  A tensor that requires grad is therefore refused
+(ValueError) unless it is detached or the call runs under ``torch.no_grad()``,
+and one with a forward-mode tangent always.
 
 Activations are bfloat16 or float32, with rows at any stride; weights and
 biases of a norm may be of the other type than its input.  Statistics, expert
