@@ -20,6 +20,8 @@ two AllReduces: ``layer_norm``, ``expert_dispatch`` / ``expert_combine`` and
 from __future__ import annotations
 
 import ctypes
+import os
+import sys
 
 from . import _lib
 from ._lib import (  # noqa: F401
@@ -32,12 +34,17 @@ __all__ = [
     "ring_ag_step", "tree_step", "hd_rs_step", "hd_ag_step", "dtree_step", "copy_", "stream_",
     "check", "chunk_range", "bind", "bind_stream", "stream_timeline",
     "context", "LIB_PATH", "predict_us", "auto_algo", "set_graphs", "set_residency_caps",
+]
+
+_OPERATORS = (
     "ExpertPlan", "layer_norm", "layer_norm_backward", "expert_dispatch",
     "expert_dispatch_backward", "expert_combine", "expert_combine_backward", "distill_loss",
     "distill_backward", "distill_step",
-]
-
-_OPERATORS = frozenset(__all__[__all__.index("ExpertPlan"):])
+)
+# ``import *`` takes the operators where there is what they need: torch (which
+# _lib has loaded then) and their binding
+if "torch" in sys.modules and os.path.exists(_lib.TORCH_OPS_PATH):
+    __all__ += _OPERATORS
 
 _ctx: dict = {}
 
@@ -51,6 +58,10 @@ def __getattr__(name):
             globals()[n] = getattr(operators, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_OPERATORS})
 
 
 def _torch():
