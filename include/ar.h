@@ -520,7 +520,7 @@ ar_status ar_expert_combine_backward(ar_ctx* ctx, const void* dy, size_t dy_stri
  * over `vocab` places (row r at r * logits_stride) and the teacher's logits
  * teacher[r][0..top) at the places indices[r][0..top) (index_bytes 4: int32,
  * 8: int64); an index outside [0, vocab) leaves its entry out.  With the
- * temperature T > 0:
+ * temperature T (positive, finite and a normal number):
  *   p = softmax(teacher / T) over the entries kept
  *   q = softmax(logits / T), lse = log(sum(exp(logits / T)))
  *   loss = T^2 * sum over entries of p * (log p - log q at their places)

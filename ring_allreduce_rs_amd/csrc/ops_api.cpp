@@ -3,6 +3,7 @@
 // norm.hip, route.hip and distill.hip.
 #include <hip/hip_runtime_api.h>
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -169,8 +170,9 @@ ar_status check_distill(ar_ctx* ctx, Arrays& arrays, arlib::DistillArgs& d, cons
         return fail(ctx, AR_ERR_UNSUPPORTED, "vocab %zu above 2^28", vocab);
     if (top > AR_DISTILL_MAX_TOP)
         return fail(ctx, AR_ERR_UNSUPPORTED, "top %zu above %d", top, AR_DISTILL_MAX_TOP);
-    if (!(temperature > 0.0f) || std::isinf(temperature))
-        return fail(ctx, AR_ERR_INVALID_ARG, "temperature %g is not positive and finite",
+    // (the kernels multiply by log2(e) / T, which overflows below the normal numbers)
+    if (!(temperature >= FLT_MIN) || std::isinf(temperature))
+        return fail(ctx, AR_ERR_INVALID_ARG, "temperature %g is not positive, normal and finite",
                     (double)temperature);
     if (rows > 1 && stride < vocab)
         return fail(ctx, AR_ERR_INVALID_ARG, "logits_stride %zu below vocab %zu", stride, vocab);

@@ -13,6 +13,8 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cfloat>
+#include <climits>
 #include <cmath>
 #include <stdexcept>
 #include <string>
@@ -469,8 +471,8 @@ struct Distill {
             throw Refused("vocab " + std::to_string(vocab) + " is 0 or top " + std::to_string(top) +
                           " outside [1, " + std::to_string(AR_DISTILL_MAX_TOP) + "]");
         temperature = (float)number(T, "temperature");
-        if (!(temperature > 0.0f) || std::isinf(temperature))
-            throw Refused("temperature is not positive and finite");
+        if (!(temperature >= FLT_MIN) || std::isinf(temperature))
+            throw Refused("temperature is not positive, normal and finite");
         stride = row_stride(logits, "logits");
     }
     const float* per_row(PyObject* o, const char* name) const {

@@ -1,12 +1,14 @@
 // launch_driver.cpp -- runs the training operators' launchers (norm.hip,
-// route.hip, distill.hip, host side only) against a HIP runtime that records
-// each launch instead of running it.  Test infrastructure only: prints "ALL OK"
-// and exits 0 when every check of the section named on the command line passes.
+// route.hip, distill.hip, host side only) and C entry points against the fake
+// HIP runtime, recording each launch instead of running it.  Test
+// infrastructure only: prints "ALL OK" and exits 0 when every check of the
+// section named on the command line passes.
 //
 // Every launch of every section has to be one that HIP accepts: blocks of
 // 1 .. 1024 threads, fewer than 2^32 threads in each dimension of the grid.
 #include <hip/hip_runtime_api.h>
 
+#include <cfloat>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -14,6 +16,8 @@
 #include <string>
 #include <vector>
 
+#include "ar.h"
+#include "fake_hip.h"
 #include "ops.h"
 
 namespace {
@@ -43,7 +47,6 @@ int g_fail = 0;
 }  // namespace
 
 extern "C" {
-hipError_t hipGetLastError() { return hipSuccess; }
 hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t lds, hipStream_t) {
     g_call = Launch{"", grid, block, lds};
     return hipSuccess;
@@ -133,11 +136,43 @@ void widths() {
             }
 }
 
+// A context on the fake device, whose memory starts at array().
+struct Device {
+    ar_ctx* ctx = nullptr;
+    Device() {
+        fake_register(array(), size_t(1) << 42, 0);
+        CHECK(ar_create(&ctx, 0, nullptr) == AR_OK);
+    }
+    ~Device() { ar_destroy(ctx); }
+};
+// Byte i GiB into the device's memory.
+template <class T = void>
+T* at(size_t i) {
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(array()) + (i << 30));
+}
+
+// 1 / T has to be a number that fp32 holds.
+void temperatures() {
+    Device d;
+    for (const float t : {FLT_MIN, 1.0f, FLT_MAX, FLT_MIN / 2, FLT_MIN / 8388608}) {
+        const ar_status want = t < FLT_MIN ? AR_ERR_INVALID_ARG : AR_OK;
+        g_launches.clear();
+        CHECK(ar_distill_loss(d.ctx, at(0), 100, at(1), 8, at(2), 4, 100, 3, AR_FLOAT32, t,
+                              at<float>(3), at<float>(4), at(5), 1 << 20) == want);
+        CHECK(ar_distill_backward(d.ctx, at<float>(3), at(0), 100, at(1), 8, at(2), at<float>(4), 4,
+                                  100, 3, AR_FLOAT32, t, at(5)) == want);
+        CHECK(ar_distill_step(d.ctx, at<float>(3), at(0), 100, at(1), 8, at(2), 4, 100, 3, AR_FLOAT32,
+                              t, at<float>(4), at(5), at(6), 1 << 20) == want);
+        CHECK(g_launches.empty() == (want != AR_OK));
+    }
+}
+
 struct Section {
     const char* name;
     void (*run)();
 };
-const Section kSections[] = {{"rows", rows}, {"widths", widths}};
+const Section kSections[] = {
+    {"rows", rows}, {"widths", widths}, {"temperatures", temperatures}};
 
 }  // namespace
 

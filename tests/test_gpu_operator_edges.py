@@ -119,3 +119,14 @@ def test_large_logits_beside_an_infinite_one(rows, vocab, t):
         ref.close(d[:, :2], -p, tol)
         rest = torch.cat([d[:, 2:vocab // 2], d[:, vocab // 2 + 1:]], 1)
         assert not rest.any()
+
+
+def test_temperatures_whose_inverse_overflows():
+    logits, at, teacher, dloss = distill_case(3, 50, 2, F32, 1)
+    lse = torch.zeros(3, device="cuda")
+    for T in (1e-40, 1e-45):
+        for call in (lambda: ar.distill_loss(logits, at, teacher, T),
+                     lambda: ar.distill_backward(dloss, logits, at, teacher, lse, T),
+                     lambda: ar.distill_step(dloss, logits, at, teacher, T)):
+            with pytest.raises(ValueError, match="temperature"):
+                call()

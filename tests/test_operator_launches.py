@@ -1,6 +1,7 @@
 """The launches of the training operators, on the host: the launchers of
-norm.hip, route.hip and distill.hip under the host sanitizers, with a HIP
-runtime that records launches (tests/host_fake/launch_driver.cpp)."""
+norm.hip, route.hip and distill.hip and the C entry points under the host
+sanitizers, with a HIP runtime that records launches
+(tests/host_fake/launch_driver.cpp)."""
 
 import os
 import shutil
@@ -26,8 +27,9 @@ def driver(tmp_path_factory):
     common = ["-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-x", "hip",
               "--cuda-host-only", f"-I{ROOT}/include", f"-I{CSRC}", f"-I{FAKE}"] + SAN
     objs = []
-    for src in (os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "route.hip"),
-                os.path.join(CSRC, "distill.hip"), os.path.join(FAKE, "launch_driver.cpp")):
+    for src in (*(os.path.join(CSRC, f) for f in ("norm.hip", "route.hip", "distill.hip",
+                                                  "ops_api.cpp", "ar_api.cpp", "dispatch.hip")),
+                os.path.join(FAKE, "fake_hip.cpp"), os.path.join(FAKE, "launch_driver.cpp")):
         obj = str(tmp / (os.path.basename(src) + ".o"))
         r = subprocess.run([HIPCC] + common + ["-c", src, "-o", obj],
                            capture_output=True, text=True, timeout=300)
@@ -52,3 +54,7 @@ def test_more_rows_than_blocks(driver):
 
 def test_the_widest_rows(driver):
     driver("widths")
+
+
+def test_temperatures_whose_inverse_overflows(driver):
+    driver("temperatures")
