@@ -26,6 +26,8 @@ struct Launch {
     std::string kernel;   // mangled
     dim3 grid, block;
     size_t lds;
+    size_t parts;         // of the kernels that are told how many parts the scratch holds
+    bool is(const char* name) const { return kernel.find(name) != std::string::npos; }
 };
 // kernels by their host address (the objects register them before main, in any order)
 std::map<const void*, std::string>& names() {
@@ -48,7 +50,7 @@ int g_fail = 0;
 
 extern "C" {
 hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t lds, hipStream_t) {
-    g_call = Launch{"", grid, block, lds};
+    g_call = Launch{"", grid, block, lds, 0};
     return hipSuccess;
 }
 hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipStream_t* s) {
@@ -58,8 +60,14 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
     *s = nullptr;
     return hipSuccess;
 }
-hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void**, size_t lds, hipStream_t) {
-    g_launches.push_back({names()[f], grid, block, lds});
+hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, size_t lds,
+                           hipStream_t) {
+    Launch l{names()[f], grid, block, lds, 0};
+    if (l.is("k_norm_fold") || l.is("k_distill_part") || l.is("k_distill_lossI"))
+        l.parts = *static_cast<size_t*>(args[1]);
+    else if (l.is("k_distill_grad"))
+        l.parts = *static_cast<size_t*>(args[2]);
+    g_launches.push_back(l);
     return hipSuccess;
 }
 void** __hipRegisterFatBinary(const void*) {
@@ -167,12 +175,98 @@ void temperatures() {
     }
 }
 
+// Every kernel stays inside the scratch that its call asks for: the C calls
+// with exactly that many bytes, over the sizes where the kernels' forms change.
+void scratch() {
+    Device d;
+    const ar_dtype types[] = {AR_BFLOAT16, AR_FLOAT32};
+    size_t need = 0, seen = 0;
+    for (const ar_dtype t : types)
+        for (const size_t cols : {1, 7, 63, 64, 200, 771, 946, 1024, 2056, 4096, 5001, 8192, 16384,
+                                  16391, 70001})
+            for (const size_t rows : {0, 1, 2, 8, 9, 64, 65, 133, 700, 1021, 6416, 16384, 70000}) {
+                CHECK(ar_layer_norm_backward_workspace(rows, cols, t, &need) == AR_OK);
+                const auto ls = launches("norm gradient", [&] {
+                    return ar_layer_norm_backward(d.ctx, at(0), cols, at(100), cols, at<float>(200),
+                                                  at<float>(201), at(202), AR_FLOAT32, at(300),
+                                                  at(400), at(401), rows, cols, t, at(402), need) ==
+                                   AR_OK ? hipSuccess : hipErrorUnknown;
+                });
+                size_t parts = 0;       // what the rows' kernels leave
+                bool folded = false;
+                for (const Launch& l : ls) {
+                    if (l.is("k_norm_grad_rows") || l.is("k_norm_grad_narrow"))
+                        parts = l.grid.x > 1 ? l.grid.x : 0;
+                    if (l.is("k_norm_cols")) parts = l.grid.y;
+                    if (l.is("k_norm_fold")) {
+                        CHECK(l.parts == parts);
+                        folded = true;
+                    }
+                }
+                CHECK(parts * 2 * cols * sizeof(float) <= need);
+                CHECK(folded == (parts > 0 || rows == 0));
+                seen += folded;
+                // (none of it where the columns' sums are not wanted)
+                CHECK(ar_layer_norm_backward(d.ctx, at(0), cols, at(100), cols, at<float>(200),
+                                             at<float>(201), at(202), AR_FLOAT32, at(300), nullptr,
+                                             nullptr, rows, cols, t, nullptr, 0) == AR_OK);
+            }
+    CHECK(seen > 0);
+    seen = 0;
+    for (const int topk : {1, 2, 5, 8, 9, 100})
+        for (const int experts : {1, 7, 64, AR_MAX_EXPERTS})
+            for (const size_t tokens : {0, 1, 300, 1024, 1448, 2000, 16384, 70001, 1000000}) {
+                CHECK(ar_expert_dispatch_workspace(tokens, topk, experts, &need) == AR_OK);
+                const auto ls = launches("dispatch", [&] {
+                    return ar_expert_dispatch(d.ctx, at(0), 8, at(100), 8, tokens, topk, experts, 8,
+                                              AR_FLOAT32, at(200), at<int>(300), at<int>(301),
+                                              at<int>(302), at(303), need) == AR_OK
+                               ? hipSuccess : hipErrorUnknown;
+                });
+                unsigned blocks = 0;
+                for (const Launch& l : ls) {
+                    if (l.is("k_route_count")) blocks = l.grid.x;
+                    if (l.is("k_route_place")) CHECK(l.grid.x == blocks && blocks > 0);
+                }
+                CHECK((size_t)blocks * (experts + 1) * sizeof(int) <= need);
+                seen += blocks > 0;
+            }
+    CHECK(seen > 0);
+    seen = 0;
+    for (const ar_dtype t : types)
+        for (const size_t vocab : {1, 5, 8, 300, 1003, 4099, 8191, 32000, 50021, 65536, 65540, 131072,
+                                   131073, 200000})
+            for (const size_t rows : {0, 1, 8, 64, 65, 300, 511, 512, 2047, 7000})
+                for (const int step : {0, 1}) {
+                    CHECK(ar_distill_workspace(rows, vocab, 30, t, step, &need) == AR_OK);
+                    const auto ls = launches("distillation", [&] {
+                        const ar_status s =
+                            step ? ar_distill_step(d.ctx, at<float>(0), at(100), vocab, at(200), 8,
+                                                   at(201), rows, vocab, 30, t, 1.0f, at<float>(202),
+                                                   at(300), at(400), need)
+                                 : ar_distill_loss(d.ctx, at(100), vocab, at(200), 8, at(201), rows,
+                                                   vocab, 30, t, 1.0f, at<float>(202), at<float>(203),
+                                                   at(400), need);
+                        return s == AR_OK ? hipSuccess : hipErrorUnknown;
+                    });
+                    size_t parts = 0;
+                    for (const Launch& l : ls) {
+                        if (l.is("k_distill_part")) parts = l.parts;
+                        else if (!l.is("k_distill_rows") && !l.is("k_distill_loss_rows"))
+                            CHECK(l.parts == parts && parts > 0);
+                    }
+                    CHECK(rows * parts * 2 * sizeof(float) <= need);
+                    seen += parts > 0;
+                }
+    CHECK(seen > 0);
+}
+
 struct Section {
     const char* name;
     void (*run)();
 };
 const Section kSections[] = {
-    {"rows", rows}, {"widths", widths}, {"temperatures", temperatures}};
+    {"rows", rows}, {"widths", widths}, {"temperatures", temperatures}, {"scratch", scratch}};
 
 }  // namespace
 

@@ -58,3 +58,7 @@ def test_the_widest_rows(driver):
 
 def test_temperatures_whose_inverse_overflows(driver):
     driver("temperatures")
+
+
+def test_scratch_holds_what_the_kernels_leave(driver):
+    driver("scratch")
