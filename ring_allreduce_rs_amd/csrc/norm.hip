@@ -544,42 +544,41 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_cols(const NormGradArgs a
 }
 
 // The last step: the partial rows of a column added in a fixed order, 64
-// columns a block with its wavefronts side by side down the parts.
+// columns a block with its wavefronts side by side down the parts.  (Groups of
+// columns past a grid's x go on in its y: blocks that walk them instead took 0.5
+// us more at 6416 x 946.)
 constexpr int kFoldThreads = 1024, kFoldWaves = kFoldThreads / 64;
 __global__ __launch_bounds__(kFoldThreads) void k_norm_fold(const NormGradArgs a, size_t parts) {
     __shared__ float lds[kFoldWaves][64];
     const unsigned lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (size_t c0 = (size_t)blockIdx.x * 64; c0 < 2 * a.cols; c0 += (size_t)gridDim.x * 64) {
-        const size_t c = c0 + lane;   // of 2 * cols
-        float s = 0.0f;
-        if (c < 2 * a.cols) {
-            constexpr int kAhead = 16;   // loads in flight
-            const float* p = a.part + c;
-            for (size_t k = wave; k < parts; k += kFoldWaves * kAhead) {
-                float v[kAhead];
+    const size_t c = ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 64 + lane;   // of 2 * cols
+    float s = 0.0f;
+    if (c < 2 * a.cols) {
+        constexpr int kAhead = 16;   // loads in flight
+        const float* p = a.part + c;
+        for (size_t k = wave; k < parts; k += kFoldWaves * kAhead) {
+            float v[kAhead];
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q)
-                    v[q] = k + q * kFoldWaves < parts ? p[(k + q * kFoldWaves) * 2 * a.cols] : 0.0f;
+            for (int q = 0; q < kAhead; ++q)
+                v[q] = k + q * kFoldWaves < parts ? p[(k + q * kFoldWaves) * 2 * a.cols] : 0.0f;
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) s += v[q];
-            }
+            for (int q = 0; q < kAhead; ++q) s += v[q];
         }
-        lds[wave][lane] = s;
-        __syncthreads();
-        if (wave == 0 && c < 2 * a.cols) {
-#pragma unroll
-            for (int w = 1; w < kFoldWaves; ++w) s += lds[w][lane];
-            void* out = c < a.cols ? a.dweight : a.dbias;
-            if (out) st_param(out, a.pb, c < a.cols ? c : c - a.cols, s);
-        }
-        __syncthreads();   // lds is free again
     }
+    lds[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= 2 * a.cols) return;
+#pragma unroll
+    for (int w = 1; w < kFoldWaves; ++w) s += lds[w][lane];
+    void* out = c < a.cols ? a.dweight : a.dbias;
+    if (out) st_param(out, a.pb, c < a.cols ? c : c - a.cols, s);
 }
 
 }  // namespace
 
-// Blocks of a launch over rows (or groups of columns): the kernels walk the
-// rest (a grid holds fewer than 2^32 threads, a block up to 2^10 of them).
+// Blocks of a launch in one dimension, of those that its rows (or groups of
+// columns) would take: a grid holds fewer than 2^32 threads, a block up to 2^10
+// of them.  The row kernels walk the rest.
 static unsigned row_blocks(size_t blocks) {
     constexpr size_t kMost = size_t(1) << 21;
     return (unsigned)(blocks < kMost ? blocks : kMost);
@@ -730,8 +729,10 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     if (!a.dweight && !a.dbias) return hipSuccess;
-    hipLaunchKernelGGL(k_norm_fold, dim3(row_blocks((2 * a.cols + 63) / 64)), dim3(kFoldThreads), 0,
-                       s, a, parts);
+    const size_t groups = (2 * a.cols + 63) / 64;
+    const unsigned gx = row_blocks(groups);
+    hipLaunchKernelGGL(k_norm_fold, dim3(gx, (unsigned)((groups + gx - 1) / gx)),
+                       dim3(kFoldThreads), 0, s, a, parts);
     return hipGetLastError();
 }
 
