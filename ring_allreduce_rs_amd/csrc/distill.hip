@@ -433,10 +433,11 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(const DistillArgs a, 
 // row may fill most of its registers.
 //
 // Thread j keeps teacher entry j of the row (a block has a thread for each); the
-// next row's entries are loaded among its units.  There is one barrier a row: before it every wavefront leaves its sums
-// of this row, after it the entries' places of the row before are written again
-// with q - p (its plain gradients were all stored before the barrier) and its
-// loss is added up.  What one row leaves in LDS the next but one replaces.
+// next row's entries are loaded among its units.  There is one barrier a row:
+// before it every wavefront leaves its sums of this row, after it the entries'
+// places of the row before are written again with q - p (its plain gradients
+// were all stored before the barrier) and its loss is added up.  What one row
+// leaves in LDS the next but one replaces.
 struct RowSums {
     float m[16], s[16], tm[16], ts[16], loss[16];
 };
