@@ -420,8 +420,10 @@ ar_status ar_check_noalloc(ar_ctx* ctx, void* const* bufs, int nranks, size_t co
 /* ------------------------------------------------------- training operators
  *
  * Operators of the networks whose gradient buckets the collectives above
- * reduce: layer norm, tokens sorted by expert and back, and distillation from
- * a teacher's top logits, each with its gradient.  Conventions:
+ * reduce: embedding, layer norm, tokens sorted by expert and back, the experts'
+ * products, their gated activation with a checkpoint in 8 bits, and
+ * distillation from a teacher's top logits, each with its gradient.
+ * Conventions:
  *  - Every array is DEVICE memory of the context's device, naturally aligned
  *    (any element-aligned address is accepted).  Sizes and strides are in
  *    elements.  Inputs with a stride argument hold row r at r * stride
@@ -556,6 +558,97 @@ ar_status ar_distill_step(ar_ctx* ctx, const float* dloss, const void* logits,
                           void* workspace, size_t workspace_bytes);
 ar_status ar_distill_workspace(size_t rows, size_t vocab, size_t top, ar_dtype dtype, int gradient,
                                size_t* bytes);
+
+/* Embedding: y[t] = scale * table[ids[t]] for `tokens` ids (index_bytes 4:
+ * int32, 8: int64), zeros where an id lies outside [0, vocab).  table: vocab
+ * rows of `hidden` elements; y: tokens rows.  The product is rounded once.
+ * scale is finite.  vocab and hidden > 0; tokens == 0 is a successful no-op.
+ * Limits (AR_ERR_UNSUPPORTED): vocab and hidden <= 2^28, tokens <= 2^31 - 1. */
+ar_status ar_embedding(ar_ctx* ctx, const void* table, const void* ids, int index_bytes,
+                       size_t tokens, size_t vocab, size_t hidden, ar_dtype dtype, float scale,
+                       void* y);
+
+/* Its gradient, dense as a bucket of the AllReduce is:
+ *   dtable[v] = scale * sum over t with ids[t] == v of dy[t]
+ * zeros in the rows of tokens that do not occur (all of them with tokens ==
+ * 0); ids outside [0, vocab) count for nothing.  The tokens are sorted by id:
+ * a row's sum is binary32 and the same bits each time. */
+ar_status ar_embedding_backward(ar_ctx* ctx, const void* dy, size_t dy_stride, const void* ids,
+                                int index_bytes, size_t tokens, size_t vocab, size_t hidden,
+                                ar_dtype dtype, float scale, void* dtable, void* workspace,
+                                size_t workspace_bytes);
+ar_status ar_embedding_backward_workspace(size_t tokens, size_t vocab, size_t hidden, ar_dtype dtype,
+                                          size_t* bytes);
+
+/* The experts' products on the rows of a dispatch.  Expert e has the rows
+ * [offsets[e], offsets[e + 1]) of `nrows` (offsets: int32, experts + 1, as
+ * ar_expert_dispatch leaves them; values outside [0, nrows] count as the nearer
+ * end) and the weights W_e = weights[e], out x hidden:
+ *   y[j] = rows[j] W_e^T                     rows: nrows x hidden, y: nrows x out
+ * and zeros in the rows from offsets[experts] on, whatever they hold.  Sums are
+ * binary32, rounded once to dtype.  hidden, out and experts > 0; nrows == 0 is
+ * a successful no-op.  Limits (AR_ERR_UNSUPPORTED): experts <= AR_MAX_EXPERTS,
+ * hidden and out <= 2^28, nrows <= 2^31 - 1. */
+ar_status ar_expert_matmul(ar_ctx* ctx, const void* rows, size_t rows_stride, const void* weights,
+                           const int* offsets, size_t nrows, int experts, size_t hidden, size_t out,
+                           ar_dtype dtype, void* y, void* workspace, size_t workspace_bytes);
+
+/* Its gradient by the rows: drows[j] = dy[j] W_e, zeros behind the last expert. */
+ar_status ar_expert_matmul_drows(ar_ctx* ctx, const void* dy, size_t dy_stride, const void* weights,
+                                 const int* offsets, size_t nrows, int experts, size_t hidden,
+                                 size_t out, ar_dtype dtype, void* drows, void* workspace,
+                                 size_t workspace_bytes);
+
+/* Its gradient by the weights: dweights[e] = sum over the rows j of expert e of
+ * dy[j]^T rows[j], zeros for an expert without rows (all of them with nrows ==
+ * 0). */
+ar_status ar_expert_matmul_dweights(ar_ctx* ctx, const void* dy, size_t dy_stride, const void* rows,
+                                    size_t rows_stride, const int* offsets, size_t nrows,
+                                    int experts, size_t hidden, size_t out, ar_dtype dtype,
+                                    void* dweights, void* workspace, size_t workspace_bytes);
+
+/* What each of the three takes as workspace. */
+typedef enum ar_expert_product {
+    AR_EXPERT_FORWARD = 0,
+    AR_EXPERT_DROWS = 1,
+    AR_EXPERT_DWEIGHTS = 2
+} ar_expert_product;
+ar_status ar_expert_matmul_workspace(ar_expert_product product, size_t nrows, int experts,
+                                     size_t hidden, size_t out, ar_dtype dtype, size_t* bytes);
+
+/* Checkpoints of activations in 8 bits.  A row of `cols` values has `cols`
+ * codes and, for each group of AR_SAVE_GROUP of them, one scale (the row's last
+ * group may be shorter):
+ *   value = code * 2^(scale - 127), code in [-127, 127]
+ * where 2^(scale - 127) is the least power of two, 2^-126 at least, with 127 *
+ * 2^(scale - 127) >= the group's largest magnitude, and code is the value over
+ * it to the nearest, ties to even (from -63 to 63 where the scale is 2^122, so
+ * that no value read back is infinite).  A group with an infinity or a NaN has
+ * scale 255 and codes 0, and reads back as NaN.  Values read back are exact in
+ * bfloat16 and binary32.  cols > 0 and <= 2^28 (AR_ERR_UNSUPPORTED); rows == 0
+ * is a successful no-op.
+ * codes: rows x cols; scales: rows x ceil(cols / AR_SAVE_GROUP). */
+#define AR_SAVE_GROUP 32
+ar_status ar_save_8bit(ar_ctx* ctx, const void* x, size_t x_stride, size_t rows, size_t cols,
+                       ar_dtype dtype, signed char* codes, unsigned char* scales);
+ar_status ar_restore_8bit(ar_ctx* ctx, const signed char* codes, const unsigned char* scales,
+                          size_t rows, size_t cols, ar_dtype dtype, void* x);
+
+/* The experts' gated activation.  A row of h holds a and u, `cols` values each:
+ *   acts = a * sigmoid(a) * u
+ * and the checkpoint of h, as ar_save_8bit makes it of 2 * rows rows of `cols`
+ * (a's, then u's, of each row), is written in the same pass. */
+ar_status ar_silu_gate(ar_ctx* ctx, const void* h, size_t h_stride, size_t rows, size_t cols,
+                       ar_dtype dtype, void* acts, signed char* codes, unsigned char* scales);
+
+/* Its gradient from the checkpoint.  With a and u as it holds them and s =
+ * sigmoid(a),
+ *   dh = (dacts * u * s * (1 + a * (1 - s)), dacts * a * s)
+ * and acts = a * s * u once more, for the gradient of the weights that the
+ * activations met. */
+ar_status ar_silu_gate_backward(ar_ctx* ctx, const void* dacts, size_t dacts_stride,
+                                const signed char* codes, const unsigned char* scales, size_t rows,
+                                size_t cols, ar_dtype dtype, void* dh, void* acts);
 
 /* Static description of a status code (never NULL). */
 const char* ar_status_string(ar_status s);

@@ -13,8 +13,9 @@ The API mirrors ``torch.distributed.all_reduce`` semantics ("Allreduceï¼šå¤§æ¨¡å
 ends with the same reduced tensor), with the participants given as a list.
 
 Beside the collectives stand the operators that a training step runs between
-two AllReduces: ``layer_norm``, ``expert_dispatch`` / ``expert_combine`` and
-``distill_loss`` / ``distill_step`` with their gradients (operators.py).
+two AllReduces: ``embedding``, ``layer_norm``, ``expert_dispatch`` /
+``expert_matmul`` / ``silu_gate`` / ``expert_combine`` and ``distill_loss`` /
+``distill_step`` with their gradients (operators.py).
 """
 
 from __future__ import annotations
@@ -25,8 +26,8 @@ import sys
 
 from . import _lib
 from ._lib import (  # noqa: F401
-    ALGOS, AR_DISTILL_MAX_TOP, AR_GRAPHS_MAX_BYTES_DEFAULT, AR_MAX_EXPERTS, AR_MAX_RANKS, DTYPES,
-    EXPORTS, LIB_PATH, OPS, ArError, Context, auto_algo, chunk_range, lib, predict_us,
+    ALGOS, AR_DISTILL_MAX_TOP, AR_GRAPHS_MAX_BYTES_DEFAULT, AR_MAX_EXPERTS, AR_MAX_RANKS,
+    AR_SAVE_GROUP, DTYPES, EXPORTS, LIB_PATH, OPS, ArError, Context, auto_algo, chunk_range, lib, predict_us,
 )
 
 __all__ = [
@@ -39,7 +40,9 @@ __all__ = [
 _OPERATORS = (
     "ExpertPlan", "layer_norm", "layer_norm_backward", "expert_dispatch",
     "expert_dispatch_backward", "expert_combine", "expert_combine_backward", "distill_loss",
-    "distill_backward", "distill_step",
+    "distill_backward", "distill_step", "embedding", "embedding_backward", "expert_matmul",
+    "expert_matmul_drows", "expert_matmul_dweights", "Saved8", "save_8bit", "restore_8bit",
+    "silu_gate", "silu_gate_backward",
 )
 # ``import *`` takes the operators where there is what they need: torch (which
 # _lib has loaded then) and their binding

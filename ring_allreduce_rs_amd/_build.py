@@ -28,7 +28,7 @@ TORCH_OPS = os.path.join(PKG, "_torch_ops.so")
 SOURCES = ["fused_f32.hip", "fused_f32_lead.hip", "fused_bf16.hip", "fused_bf16_lead.hip",
            "fused_i32.hip", "fused_i32_lead.hip", "fused.hip", "steps.hip", "copy.hip",
            "check.hip", "probe.hip", "dispatch.hip", "ar_api.cpp", "norm.hip", "route.hip",
-           "distill.hip", "ops_api.cpp"]
+           "distill.hip", "ops_api.cpp", "embed.hip", "product.hip", "gate.hip", "model_api.cpp"]
 
 FLAGS = [
     "--offload-arch=gfx950",

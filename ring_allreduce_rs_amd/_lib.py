@@ -18,6 +18,7 @@ AR_MAX_RANKS = 64
 AR_GRAPHS_MAX_BYTES_DEFAULT = 8 << 20
 AR_MAX_EXPERTS = 1024
 AR_DISTILL_MAX_TOP = 1024
+AR_SAVE_GROUP = 32
 
 AR_OK = 0
 AR_ERR_INVALID_ARG = 1
@@ -42,7 +43,10 @@ EXPORTS = (
     "ar_layer_norm_backward_workspace", "ar_expert_dispatch", "ar_expert_dispatch_workspace",
     "ar_expert_dispatch_backward", "ar_expert_combine", "ar_expert_combine_backward",
     "ar_distill_loss", "ar_distill_backward", "ar_distill_step", "ar_distill_workspace",
-    "ar_status_string",
+    "ar_embedding", "ar_embedding_backward", "ar_embedding_backward_workspace",
+    "ar_expert_matmul", "ar_expert_matmul_drows", "ar_expert_matmul_dweights",
+    "ar_expert_matmul_workspace", "ar_save_8bit", "ar_restore_8bit", "ar_silu_gate",
+    "ar_silu_gate_backward", "ar_status_string",
     "ar_last_error", "ar_destroy",
 )
 
@@ -113,6 +117,17 @@ def _load() -> ctypes.CDLL:
         "ar_distill_backward": ([vp, vp, vp, sz, vp, i, vp, vp, sz, sz, sz, i, f, vp], i),
         "ar_distill_step": ([vp, vp, vp, sz, vp, i, vp, sz, sz, sz, i, f, vp, vp, vp, sz], i),
         "ar_distill_workspace": ([sz, sz, sz, i, i, psz], i),
+        "ar_embedding": ([vp, vp, vp, i, sz, sz, sz, i, f, vp], i),
+        "ar_embedding_backward": ([vp, vp, sz, vp, i, sz, sz, sz, i, f, vp, vp, sz], i),
+        "ar_embedding_backward_workspace": ([sz, sz, sz, i, psz], i),
+        "ar_expert_matmul": ([vp, vp, sz, vp, vp, sz, i, sz, sz, i, vp, vp, sz], i),
+        "ar_expert_matmul_drows": ([vp, vp, sz, vp, vp, sz, i, sz, sz, i, vp, vp, sz], i),
+        "ar_expert_matmul_dweights": ([vp, vp, sz, vp, sz, vp, sz, i, sz, sz, i, vp, vp, sz], i),
+        "ar_expert_matmul_workspace": ([i, sz, i, sz, sz, i, psz], i),
+        "ar_save_8bit": ([vp, vp, sz, sz, sz, i, vp, vp], i),
+        "ar_restore_8bit": ([vp, vp, vp, sz, sz, i, vp], i),
+        "ar_silu_gate": ([vp, vp, sz, sz, sz, i, vp, vp, vp], i),
+        "ar_silu_gate_backward": ([vp, vp, sz, vp, vp, sz, sz, i, vp, vp], i),
         "ar_status_string": ([i], cp),
         "ar_last_error": ([vp], cp),
         "ar_destroy": ([vp], i),

@@ -531,12 +531,269 @@ PyObject* distill_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// ------------------------------------------------------------------------- embedding
+
+// ids: any shape, dense, on like's device.
+const void* token_ids(const at::Tensor& ids, const at::Tensor& like, int* ib) {
+    *ib = index_bytes(ids, "ids");
+    return dense(ids, "ids", ids.scalar_type(), ids.sizes(), like);
+}
+
+float finite(PyObject* o, const char* name) {
+    const float v = (float)number(o, name);
+    if (!std::isfinite(v)) throw Refused(std::string(name) + " is not finite");
+    return v;
+}
+
+PyObject* embedding(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        ar_dtype dt;
+        int ib;
+        const at::Tensor& table = floats(args[0], "table", &dt);
+        if (table.dim() != 2 || table.size(0) == 0 || table.size(1) == 0)
+            throw Refused("table has shape " + shape_of(table) + ", needs (vocab, hidden)");
+        if (!table.is_contiguous()) throw Refused("table is not contiguous");
+        const at::Tensor& ids = tensor(args[1], "ids");
+        const void* i = token_ids(ids, table, &ib);
+        const float scale = finite(args[2], "scale");
+        c10::SmallVector<int64_t, 6> shape(ids.sizes().begin(), ids.sizes().end());
+        shape.push_back(table.size(1));
+        at::Tensor y = make(shape, table.scalar_type(), table);
+        ar_ctx* c = context(table.get_device());
+        must(c, ar_embedding(c, table.data_ptr(), i, ib, (size_t)ids.numel(), (size_t)table.size(0),
+                             (size_t)table.size(1), dt, scale, y.data_ptr()), "ar_embedding");
+        return THPVariable_Wrap(y);
+    });
+}
+
+PyObject* embedding_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(n, 4, [&]() -> PyObject* {
+        ar_dtype dt;
+        int ib;
+        const at::Tensor& dy = floats(args[0], "dy", &dt);
+        const at::Tensor& ids = tensor(args[1], "ids");
+        const void* i = token_ids(ids, dy, &ib);
+        if (dy.dim() != ids.dim() + 1 || dy.sizes().slice(0, ids.dim()) != ids.sizes() ||
+            dy.size(-1) == 0)
+            throw Refused("dy " + shape_of(dy) + " does not match ids " + shape_of(ids));
+        const int64_t vocab = whole(args[2], "vocab"), hidden = dy.size(-1);
+        if (vocab < 1) throw Refused("vocab " + std::to_string(vocab) + " below 1");
+        const float scale = finite(args[3], "scale");
+        const int64_t stride = row_stride(dy, "dy");
+        const size_t tokens = (size_t)ids.numel();
+        size_t bytes = 0;
+        must(nullptr, ar_embedding_backward_workspace(tokens, (size_t)vocab, (size_t)hidden, dt,
+                                                      &bytes), "ar_embedding_backward_workspace");
+        at::Tensor dtable = make({vocab, hidden}, dy.scalar_type(), dy);
+        const Scratch ws(bytes, dy);
+        ar_ctx* c = context(dy.get_device());
+        must(c, ar_embedding_backward(c, dy.data_ptr(), (size_t)stride, i, ib, tokens, (size_t)vocab,
+                                      (size_t)hidden, dt, scale, dtable.data_ptr(), ws.p, ws.bytes),
+             "ar_embedding_backward");
+        return THPVariable_Wrap(dtable);
+    });
+}
+
+// ------------------------------------------------------------------ the experts' products
+
+// The rows of a product: a matrix with rows at any stride.
+struct Rows {
+    const at::Tensor& t;
+    ar_dtype dt;
+    int64_t stride;
+    Rows(PyObject* o, const char* name) : t(floats(o, name, &dt)) {
+        if (t.dim() != 2 || t.size(1) == 0)
+            throw Refused(std::string(name) + " has shape " + shape_of(t) + ", needs (rows, width)");
+        stride = row_stride(t, name);
+    }
+};
+
+const int* plan_offsets(PyObject* o, const at::Tensor& like, int64_t* experts) {
+    const at::Tensor& t = tensor(o, "plan.offsets");
+    if (t.dim() != 1 || t.size(0) < 2)
+        throw Refused("plan.offsets has shape " + shape_of(t) + ", needs (experts + 1,)");
+    *experts = t.size(0) - 1;
+    check_experts(*experts);
+    return static_cast<const int*>(dense(t, "plan.offsets", at::kInt, t.sizes(), like));
+}
+
+size_t product_workspace(ar_expert_product p, int64_t rows, int64_t experts, int64_t hidden,
+                         int64_t out, ar_dtype dt) {
+    size_t bytes = 0;
+    must(nullptr, ar_expert_matmul_workspace(p, (size_t)rows, (int)experts, (size_t)hidden,
+                                             (size_t)out, dt, &bytes), "ar_expert_matmul_workspace");
+    return bytes;
+}
+
+// ar_expert_matmul (KIND AR_EXPERT_FORWARD) or ar_expert_matmul_drows
+template <ar_expert_product KIND>
+PyObject* product_of_rows(PyObject* const* args, Py_ssize_t n, const char* name) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        constexpr bool kForward = KIND == AR_EXPERT_FORWARD;
+        const Rows r(args[0], name);
+        const at::Tensor& w = tensor(args[1], "weights");
+        if (w.dim() != 3 || w.size(1) == 0 || w.size(2) == 0)
+            throw Refused("weights has shape " + shape_of(w) + ", needs (experts, out, hidden)");
+        const int64_t out = w.size(1), hidden = w.size(2), rows = r.t.size(0);
+        const void* wp = dense(w, "weights", r.t.scalar_type(), w.sizes(), r.t);
+        if (r.t.size(1) != (kForward ? hidden : out))
+            throw Refused(std::string(name) + " " + shape_of(r.t) + " does not match weights " +
+                          shape_of(w));
+        int64_t experts;
+        const int* offsets = plan_offsets(args[2], r.t, &experts);
+        if (experts != w.size(0))
+            throw Refused("weights " + shape_of(w) + " are not of the plan's " +
+                          std::to_string(experts) + " experts");
+        at::Tensor y = make({rows, kForward ? out : hidden}, r.t.scalar_type(), r.t);
+        const Scratch ws(product_workspace(KIND, rows, experts, hidden, out, r.dt), r.t);
+        ar_ctx* c = context(r.t.get_device());
+        must(c, (kForward ? ar_expert_matmul : ar_expert_matmul_drows)(
+                    c, r.t.data_ptr(), (size_t)r.stride, wp, offsets, (size_t)rows, (int)experts,
+                    (size_t)hidden, (size_t)out, r.dt, y.data_ptr(), ws.p, ws.bytes),
+             kForward ? "ar_expert_matmul" : "ar_expert_matmul_drows");
+        return THPVariable_Wrap(y);
+    });
+}
+
+PyObject* expert_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return product_of_rows<AR_EXPERT_FORWARD>(args, n, "rows");
+}
+
+PyObject* expert_matmul_drows(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return product_of_rows<AR_EXPERT_DROWS>(args, n, "dout");
+}
+
+PyObject* expert_matmul_dweights(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const Rows d(args[0], "dout"), r(args[1], "rows");
+        if (d.dt != r.dt || d.t.size(0) != r.t.size(0) || d.t.device() != r.t.device())
+            throw Refused("dout " + shape_of(d.t) + " does not match rows " + shape_of(r.t) +
+                          " in dtype, rows or device");
+        int64_t experts;
+        const int* offsets = plan_offsets(args[2], r.t, &experts);
+        const int64_t rows = r.t.size(0), hidden = r.t.size(1), out = d.t.size(1);
+        const size_t bytes = product_workspace(AR_EXPERT_DWEIGHTS, rows, experts, hidden, out, r.dt);
+        at::Tensor dw = make({experts, out, hidden}, r.t.scalar_type(), r.t);
+        const Scratch ws(bytes, r.t);
+        ar_ctx* c = context(r.t.get_device());
+        must(c, ar_expert_matmul_dweights(c, d.t.data_ptr(), (size_t)d.stride, r.t.data_ptr(),
+                                          (size_t)r.stride, offsets, (size_t)rows, (int)experts,
+                                          (size_t)hidden, (size_t)out, r.dt, dw.data_ptr(), ws.p,
+                                          ws.bytes), "ar_expert_matmul_dweights");
+        return THPVariable_Wrap(dw);
+    });
+}
+
+// ------------------------------------------------------ checkpoints in 8 bits and the gate
+
+int64_t groups_of(int64_t cols) { return (cols + AR_SAVE_GROUP - 1) / AR_SAVE_GROUP; }
+
+// The shape `lead` + the given dimensions.
+template <class... N>
+c10::SmallVector<int64_t, 6> shape_with(at::IntArrayRef lead, N... n) {
+    c10::SmallVector<int64_t, 6> s(lead.begin(), lead.end());
+    (s.push_back(n), ...);
+    return s;
+}
+
+// A checkpoint's tensors; its rows have to be dense.
+struct Saved {
+    const at::Tensor& codes;
+    signed char* c;
+    unsigned char* s;
+    Saved(PyObject* co, PyObject* so) : codes(tensor(co, "saved.codes")) {
+        if (!codes.is_cuda()) throw Refused("saved.codes is not on a GPU");
+        if (codes.dim() == 0 || codes.size(-1) == 0)
+            throw Refused("saved.codes has shape " + shape_of(codes) + ", needs (..., values)");
+        c = static_cast<signed char*>(dense(codes, "saved.codes", at::kChar, codes.sizes(), codes));
+        s = static_cast<unsigned char*>(
+            dense(tensor(so, "saved.scales"), "saved.scales", at::kByte,
+                  shape_with(codes.sizes().slice(0, codes.dim() - 1), groups_of(codes.size(-1))),
+                  codes));
+    }
+};
+
+PyObject* save_8bit(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(n, 1, [&]() -> PyObject* {
+        ar_dtype dt;
+        const at::Tensor& x = floats(args[0], "x", &dt);
+        const int64_t stride = row_stride(x, "x"), cols = x.size(-1);
+        if (cols == 0) throw Refused("x has rows of no elements");
+        at::Tensor codes = make(x.sizes(), at::kChar, x);
+        at::Tensor scales =
+            make(shape_with(x.sizes().slice(0, x.dim() - 1), groups_of(cols)), at::kByte, x);
+        ar_ctx* c = context(x.get_device());
+        must(c, ar_save_8bit(c, x.data_ptr(), (size_t)stride, (size_t)(x.numel() / cols),
+                             (size_t)cols, dt, static_cast<signed char*>(codes.data_ptr()),
+                             static_cast<unsigned char*>(scales.data_ptr())), "ar_save_8bit");
+        return tuple_of(codes, scales);
+    });
+}
+
+PyObject* restore_8bit(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const Saved v(args[0], args[1]);
+        const int64_t eb = whole(args[2], "dtype"), cols = v.codes.size(-1);
+        if (eb != 2 && eb != 4) throw Refused("dtype is neither bfloat16 nor float32");
+        at::Tensor x = make(v.codes.sizes(), eb == 2 ? at::kBFloat16 : at::kFloat, v.codes);
+        ar_ctx* c = context(x.get_device());
+        must(c, ar_restore_8bit(c, v.c, v.s, (size_t)(x.numel() / cols), (size_t)cols,
+                                eb == 2 ? AR_BFLOAT16 : AR_FLOAT32, x.data_ptr()),
+             "ar_restore_8bit");
+        return THPVariable_Wrap(x);
+    });
+}
+
+PyObject* silu_gate(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(n, 1, [&]() -> PyObject* {
+        ar_dtype dt;
+        const at::Tensor& h = floats(args[0], "h", &dt);
+        const int64_t stride = row_stride(h, "h");
+        if (h.size(-1) == 0 || h.size(-1) % 2)
+            throw Refused("h has shape " + shape_of(h) + ", needs (..., 2 n)");
+        const int64_t cols = h.size(-1) / 2, rows = h.numel() / (2 * cols);
+        const at::IntArrayRef lead = h.sizes().slice(0, h.dim() - 1);
+        at::Tensor acts = make(shape_with(lead, cols), h.scalar_type(), h);
+        at::Tensor codes = make(shape_with(lead, 2, cols), at::kChar, h);
+        at::Tensor scales = make(shape_with(lead, 2, groups_of(cols)), at::kByte, h);
+        ar_ctx* c = context(h.get_device());
+        must(c, ar_silu_gate(c, h.data_ptr(), (size_t)stride, (size_t)rows, (size_t)cols, dt,
+                             acts.data_ptr(), static_cast<signed char*>(codes.data_ptr()),
+                             static_cast<unsigned char*>(scales.data_ptr())), "ar_silu_gate");
+        return tuple_of(acts, codes, scales);
+    });
+}
+
+PyObject* silu_gate_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        ar_dtype dt;
+        const at::Tensor& d = floats(args[0], "dacts", &dt);
+        const int64_t stride = row_stride(d, "dacts"), cols = d.size(-1);
+        const Saved v(args[1], args[2]);
+        const at::IntArrayRef lead = d.sizes().slice(0, d.dim() - 1);
+        if (v.codes.sizes() != at::IntArrayRef(shape_with(lead, 2, cols)))
+            throw Refused("saved.codes " + shape_of(v.codes) + " does not match dacts " +
+                          shape_of(d));
+        same_device(v.codes, "saved.codes", d);
+        at::Tensor dh = make(shape_with(lead, 2 * cols), d.scalar_type(), d);
+        at::Tensor acts = make(d.sizes(), d.scalar_type(), d);
+        ar_ctx* c = context(d.get_device());
+        must(c, ar_silu_gate_backward(c, d.data_ptr(), (size_t)stride, v.c, v.s,
+                                      (size_t)(d.numel() / cols), (size_t)cols, dt, dh.data_ptr(),
+                                      acts.data_ptr()), "ar_silu_gate_backward");
+        return tuple_of(dh, acts);
+    });
+}
+
 #define ENTRY(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {
     ENTRY(layer_norm),      ENTRY(layer_norm_backward),     ENTRY(expert_dispatch),
     ENTRY(expert_combine),  ENTRY(expert_dispatch_backward), ENTRY(expert_combine_backward),
     ENTRY(distill_loss),    ENTRY(distill_backward),        ENTRY(distill_step),
+    ENTRY(embedding),       ENTRY(embedding_backward),      ENTRY(expert_matmul),
+    ENTRY(expert_matmul_drows), ENTRY(expert_matmul_dweights), ENTRY(save_8bit),
+    ENTRY(restore_8bit),    ENTRY(silu_gate),               ENTRY(silu_gate_backward),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -1,5 +1,7 @@
-"""Training operators on torch tensors: layer norm, tokens sorted by expert and
-back, and distillation from a teacher's top logits, each with its gradient.
+"""Training operators on torch tensors: embedding, layer norm, tokens sorted by
+expert and back, the experts' products and their gated activation with a
+checkpoint in 8 bits, and distillation from a teacher's top logits, each with
+its gradient.
 
 They are the operators beside the collectives in a data-parallel training
 step: what the forward and backward passes run between two AllReduces of the
@@ -8,7 +10,8 @@ outputs (and scratch, where an operator needs some) from torch's allocator, and
 enqueues the HIP kernels of libar.so on torch's current stream (include/ar.h
 holds the formulas and limits; csrc/torch_ops.cpp is the binding).  Nothing is
 recorded for torch's autograd: the gradients are the ``*_backward`` functions
-(and ``distill_step``).  A tensor that requires grad is therefore refused
+(``expert_matmul_drows`` and ``expert_matmul_dweights`` for the products, and
+``distill_step``).  A tensor that requires grad is therefore refused
 (ValueError) unless it is detached or the call runs under ``torch.no_grad()``,
 and one with a forward-mode tangent always.
 
@@ -111,3 +114,72 @@ def distill_step(dloss, logits, indices, teacher, temperature: float = 1.0):
     """Loss and gradient at once, where each row's dloss is known beforehand (a
     mean over the batch, say): (loss, dlogits)."""
     return _ops.distill_step(dloss, logits, indices, teacher, temperature)
+
+
+def embedding(table, ids, scale: float = 1.0):
+    """scale * table[ids]: the rows of table (vocab, hidden) by token, ids (int32
+    or int64) of any shape.  An id outside [0, vocab) gives a row of zeros."""
+    return _ops.embedding(table, ids, scale)
+
+
+def embedding_backward(dy, ids, vocab: int, scale: float = 1.0):
+    """Gradient of ``embedding``'s table, dense: (vocab, hidden) of dy's dtype,
+    zeros in the rows of tokens that do not occur.  The tokens are sorted by id,
+    so the sums repeat to the bit."""
+    return _ops.embedding_backward(dy, ids, vocab, scale)
+
+
+def expert_matmul(rows, weights, plan: ExpertPlan):
+    """Each expert's product with its own rows of a dispatch: rows (n, hidden) and
+    weights (experts, out, hidden) give (n, out), out[j] = rows[j] @
+    weights[e].T for the rows j of expert e; zeros in the rows without one."""
+    return _ops.expert_matmul(rows, weights, plan[2])
+
+
+def expert_matmul_drows(dout, weights, plan: ExpertPlan):
+    """Gradient of ``expert_matmul``'s rows: dout[j] @ weights[e]."""
+    return _ops.expert_matmul_drows(dout, weights, plan[2])
+
+
+def expert_matmul_dweights(dout, rows, plan: ExpertPlan):
+    """Gradient of ``expert_matmul``'s weights, of the rows' dtype: for each expert
+    dout[j].T @ rows[j] over its rows, zeros without any."""
+    return _ops.expert_matmul_dweights(dout, rows, plan[2])
+
+
+class Saved8(NamedTuple):
+    """A checkpoint in 8 bits: value = code * 2**(scale - 127).
+
+    codes   int8, the values' shape
+    scales  uint8, one for each 32 values along the last dimension
+    """
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def save_8bit(x):
+    """x in 8 bits, groups of 32 along the last dimension sharing a power of two as
+    their scale: each value is off by half a scale at most, which is no more
+    than the group's largest magnitude over 127."""
+    return Saved8(*_ops.save_8bit(x))
+
+
+def restore_8bit(saved: Saved8, dtype=torch.bfloat16):
+    """The values of a checkpoint, exactly, as bfloat16 or float32."""
+    return _ops.restore_8bit(saved[0], saved[1], 4 if dtype == torch.float32 else
+                             2 if dtype == torch.bfloat16 else 0)
+
+
+def silu_gate(h):
+    """The experts' gated activation: h (..., 2 n) holds a and u, and acts (..., n)
+    is a * sigmoid(a) * u.  Returns (acts, saved): saved is the checkpoint of
+    h.view(..., 2, n), all that ``silu_gate_backward`` needs of h."""
+    acts, codes, scales = _ops.silu_gate(h)
+    return acts, Saved8(codes, scales)
+
+
+def silu_gate_backward(dacts, saved: Saved8):
+    """Gradient of ``silu_gate`` at the checkpoint's values: (dh, acts), the
+    activations once more for ``expert_matmul_dweights``."""
+    return _ops.silu_gate_backward(dacts, saved[0], saved[1])
