@@ -583,12 +583,12 @@ ar_status ar_embedding_backward_workspace(size_t tokens, size_t vocab, size_t hi
 /* The experts' products on the rows of a dispatch.  Expert e has the rows
  * [offsets[e], offsets[e + 1]) of `nrows` (offsets: int32, experts + 1, as
  * ar_expert_dispatch leaves them; values outside [0, nrows] count as the nearer
- * end) and the weights W_e = weights[e], out x hidden:
+ * end, the first as 0) and the weights W_e = weights[e], out x hidden:
  *   y[j] = rows[j] W_e^T                     rows: nrows x hidden, y: nrows x out
  * and zeros in the rows from offsets[experts] on, whatever they hold.  Sums are
  * binary32, rounded once to dtype.  hidden, out and experts > 0; nrows == 0 is
  * a successful no-op.  Limits (AR_ERR_UNSUPPORTED): experts <= AR_MAX_EXPERTS,
- * hidden and out <= 2^28, nrows <= 2^31 - 1. */
+ * hidden, out and the strides <= 2^20, nrows <= 2^31 - 1. */
 ar_status ar_expert_matmul(ar_ctx* ctx, const void* rows, size_t rows_stride, const void* weights,
                            const int* offsets, size_t nrows, int experts, size_t hidden, size_t out,
                            ar_dtype dtype, void* y, void* workspace, size_t workspace_bytes);

@@ -52,6 +52,10 @@ ar_status check_embed(ar_ctx* ctx, int index_bytes, size_t tokens, size_t vocab,
     return AR_OK;
 }
 
+// Widest rows of a product, and furthest apart: the rows of a tile span less than
+// 2^31 bytes.
+constexpr size_t kMostWide = size_t(1) << 20;
+
 // Whether the sizes of a product are in range; the weights' bytes.
 ar_status check_product(ar_ctx* ctx, size_t nrows, int experts, size_t hidden, size_t out, int dtype,
                         size_t* eb, size_t* wbytes) {
@@ -61,8 +65,8 @@ ar_status check_product(ar_ctx* ctx, size_t nrows, int experts, size_t hidden, s
     if (hidden < 1 || out < 1) return fail(ctx, AR_ERR_INVALID_ARG, "hidden or out is 0");
     if (experts > AR_MAX_EXPERTS)
         return fail(ctx, AR_ERR_UNSUPPORTED, "experts %d above %d", experts, AR_MAX_EXPERTS);
-    if (hidden > kMostCols || out > kMostCols)
-        return fail(ctx, AR_ERR_UNSUPPORTED, "hidden %zu or out %zu above 2^28", hidden, out);
+    if (hidden > kMostWide || out > kMostWide)
+        return fail(ctx, AR_ERR_UNSUPPORTED, "hidden %zu or out %zu above 2^20", hidden, out);
     if (nrows > (size_t)INT_MAX)
         return fail(ctx, AR_ERR_UNSUPPORTED, "nrows %zu above 2^31 - 1", nrows);
     size_t w;
@@ -78,6 +82,16 @@ ar_status check_stride(ar_ctx* ctx, const char* name, size_t rows, size_t stride
     return AR_OK;
 }
 
+// A product's stride between `rows` rows of `cols`; that of a single row is of no
+// meaning and becomes its width.
+ar_status check_product_stride(ar_ctx* ctx, const char* name, size_t rows, size_t* stride,
+                               size_t cols) {
+    if (rows <= 1) *stride = cols;
+    if (*stride > kMostWide)
+        return fail(ctx, AR_ERR_UNSUPPORTED, "%s %zu above 2^20", name, *stride);
+    return check_stride(ctx, name, rows, *stride, cols);
+}
+
 // ar_expert_matmul and ar_expert_matmul_drows: c[j] = a[j] W^T or a[j] W.
 ar_status product_rows(ar_ctx* ctx, ProductKind kind, const char* what, const void* in,
                        const char* in_name, size_t stride, const char* stride_name,
@@ -89,7 +103,7 @@ ar_status product_rows(ar_ctx* ctx, ProductKind kind, const char* what, const vo
         ar_status s = check_product(ctx, nrows, experts, hidden, out, (int)dtype, &eb, &wbytes);
         const size_t icols = kind == arlib::PRODUCT_FORWARD ? hidden : out;
         const size_t ycols = kind == arlib::PRODUCT_FORWARD ? out : hidden;
-        if (s == AR_OK) s = check_stride(ctx, stride_name, nrows, stride, icols);
+        if (s == AR_OK) s = check_product_stride(ctx, stride_name, nrows, &stride, icols);
         if (s != AR_OK) return s;
         if (!strided_bytes(nrows, icols, stride, eb, &ibytes) ||
             !strided_bytes(nrows, ycols, ycols, eb, &ybytes))
@@ -210,8 +224,8 @@ ar_status ar_expert_matmul_dweights(ar_ctx* ctx, const void* dy, size_t dy_strid
     return guarded(ctx, [&]() -> ar_status {
         size_t eb, wbytes, gbytes, rbytes;
         ar_status s = check_product(ctx, nrows, experts, hidden, out, (int)dtype, &eb, &wbytes);
-        if (s == AR_OK) s = check_stride(ctx, "dy_stride", nrows, dy_stride, out);
-        if (s == AR_OK) s = check_stride(ctx, "rows_stride", nrows, rows_stride, hidden);
+        if (s == AR_OK) s = check_product_stride(ctx, "dy_stride", nrows, &dy_stride, out);
+        if (s == AR_OK) s = check_product_stride(ctx, "rows_stride", nrows, &rows_stride, hidden);
         if (s != AR_OK) return s;
         if (!strided_bytes(nrows, out, dy_stride, eb, &gbytes) ||
             !strided_bytes(nrows, hidden, rows_stride, eb, &rbytes))
@@ -241,7 +255,7 @@ ar_status ar_expert_matmul_workspace(ar_expert_product product, size_t nrows, in
     if (!bytes || !eb || experts < 1 || hidden < 1 || out < 1 || (int)product < 0 ||
         (int)product > (int)AR_EXPERT_DWEIGHTS)
         return AR_ERR_INVALID_ARG;
-    if (experts > AR_MAX_EXPERTS || hidden > kMostCols || out > kMostCols ||
+    if (experts > AR_MAX_EXPERTS || hidden > kMostWide || out > kMostWide ||
         nrows > (size_t)INT_MAX)
         return AR_ERR_UNSUPPORTED;
     if (!times(hidden, out, &w) || !times(w, (size_t)experts, &w) || !times(w, eb, &w))

@@ -4,6 +4,7 @@
 #include "ops_device.h"
 
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 namespace arlib {
@@ -20,25 +21,23 @@ __device__ __forceinline__ T ld_lds(lds_t p) {
     return *(__attribute__((address_space(3))) const T*)p;
 }
 
-constexpr int kStep = 128;    // bytes of the reduced dimension in a step
-constexpr int kStepUnits = kStep / 16;
 
 // A tile of one operand in LDS, of T rows (or columns) of the result by one
 // step, in 16-byte units.  KC: the reduced dimension is the contiguous one in
 // memory, and the tile is [T][step]; otherwise [step][T].  Units are swapped
 // within a line so that the lanes of a wavefront read from all banks.
-template <int EB, bool KC, int T>
+template <int EB, bool KC, int T, int STEP>
 struct Tile {
     static constexpr int E = 16 / EB;
-    static constexpr int S = kStep / EB;                 // elements of a step
+    static constexpr int S = STEP / EB;                  // elements of a step of STEP bytes
     static constexpr int ROWS = KC ? T : S;
-    static constexpr int UNITS = KC ? kStepUnits : T / E;   // of a line
+    static constexpr int UNITS = KC ? STEP / 16 : T / E;   // of a line
     static constexpr int BYTES = ROWS * UNITS * 16;
 
     __device__ __forceinline__ static int swap_of(int row) {
-        if constexpr (KC) return row & 7;
-        else if constexpr (EB == 2) return 2 * ((row & 3) | ((row >> 1) & 4));
-        else return 4 * ((row >> 2) & 3);
+        if constexpr (KC) return row & (UNITS - 1);
+        else if constexpr (EB == 2) return 2 * ((row & 3) | ((row >> 1) & 4)) & (UNITS - 1);
+        else return 4 * ((row >> 2) & 3) & (UNITS - 1);
     }
     __device__ __forceinline__ static int at(int row, int unit) {
         return (row * UNITS + (unit ^ swap_of(row))) * 16;
@@ -54,7 +53,7 @@ struct Tile {
     // the buffers, and the piece's own `first` (a constant).  The swaps only change
     // bits that the lines' and buffers' addresses leave 0, so a piece's place is
     // the origin's with some bits turned over, plus a constant.
-    static constexpr int kTurn = KC ? 0 : EB == 2 ? 14 : 12;   // units that swaps reach
+    static constexpr int kTurn = (KC ? 0 : EB == 2 ? 14 : 12) & (UNITS - 1);   // units that swaps reach
     __device__ __forceinline__ static unsigned origin(int lane, int first) {
         const int i = lane & 15, g = lane >> 4;
         if constexpr (KC) return at(first + i, g);
@@ -96,6 +95,18 @@ __device__ __forceinline__ f32x4 mma(f32x4 a, f32x4 b, f32x4 c) {
     return c;
 }
 
+// What is the same on every lane, in scalar registers.
+__device__ __forceinline__ unsigned uniform(unsigned v) {
+    return (unsigned)__builtin_amdgcn_readfirstlane((int)v);
+}
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+    return (uint64_t)uniform((unsigned)(v >> 32)) << 32 | uniform((unsigned)v);
+}
+template <class T>
+__device__ __forceinline__ T* uniform(T* p) {
+    return (T*)(uintptr_t)uniform64((uint64_t)(uintptr_t)p);
+}
+
 // An operand in memory: `rows` lines of `cols` elements that may be read.
 struct Operand {
     const char* base;
@@ -103,101 +114,163 @@ struct Operand {
     unsigned rows, cols;
 };
 
-// How a tile comes from memory into LDS, a step of the reduced dimension at a
-// time.  begin() says where, aim() which step; load() starts share q of N of its
-// loads; arrive(), before the wavefronts meet, has them on their way to LDS.
+// The last `live` elements of a line of n, first in a unit with zeros behind them.
+template <int EB>
+__device__ __forceinline__ u32x4 ld_end(const char* line, unsigned n, unsigned live) {
+    constexpr unsigned E = 16 / EB;
+    if (n < E) return ld_unit_of<EB>(line, n - live, n, 0u);
+    const u32x4 u = ld_unit<EB>(line + (size_t)(n - E) * EB);
+    uint64_t lo = (uint64_t)u[1] << 32 | u[0], hi = (uint64_t)u[3] << 32 | u[2];
+    const unsigned away = (E - live) * EB * 8;    // bits, 1 .. 127
+    if (away >= 64) {
+        lo = hi >> (away - 64);
+        hi = 0;
+    } else {
+        lo = lo >> away | hi << (64 - away);
+        hi >>= away;
+    }
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
 
-// Through registers, for lines at any address.
+__device__ __forceinline__ void st_lds(lds_t p, u32x4 v) {
+    *(__attribute__((address_space(3))) u32x4*)p = v;
+}
+
+// s_waitcnt's operand for vmcnt(0) alone.
+constexpr int kVmcnt0 = 0x0f70;
+
+// How a tile comes from memory into LDS, a step of the reduced dimension at a
+// time, in 16-byte units, N a thread.  begin() says where, aim() which step;
+// load() starts the thread's unit q, and arrive(), before the wavefronts meet,
+// has the step that aim() had last on its way to LDS.
+//
+// A unit outside the operand is zeros.  So is one that a line's end cuts, where
+// what lies behind it may not be read (behind the reduced dimension, and behind
+// the operand's last line), but for the elements that belong to it.
 template <int EB, class TILE, bool KC, int NT>
-struct Through {
+struct Lines {
     static constexpr int N = TILE::ROWS * TILE::UNITS / NT;
     static_assert(TILE::ROWS * TILE::UNITS % NT == 0, "");
-    u32x4 u[N];
-    Operand o;
-    unsigned first, k;
-    __device__ __forceinline__ void begin(const Operand& op, unsigned at, unsigned) {
-        o = op;
-        first = at;
+    static constexpr unsigned E = TILE::E;
+    static constexpr unsigned kOutside = 0x80000000u;
+    const char* base;       // the tile's first line (KC), its first column's
+    unsigned off[N];        // bytes from the step's begin
+    unsigned depth, wide, high, step;
+    size_t stride;
+    // Thread t's unit q, which goes to LDS unit q * NT + t: its line, and its unit in memory.
+    __device__ __forceinline__ static unsigned line(int q, unsigned t) {
+        return ((unsigned)(q * NT) + t) / TILE::UNITS;
     }
-    __device__ __forceinline__ void end() { o.rows = 0; }
-    __device__ __forceinline__ void aim(unsigned step) { k = step; }
+    __device__ __forceinline__ static unsigned unit(int q, unsigned t) {
+        return ((unsigned)(q * NT) + t) % TILE::UNITS ^ (unsigned)TILE::swap_of((int)line(q, t));
+    }
+    __device__ __forceinline__ static lds_t slot(lds_t lds, int q, unsigned t) {
+        return lds + (q * NT + (int)t) * 16;
+    }
+    __device__ __forceinline__ void begin(const Operand& o, unsigned first, unsigned depth_) {
+        depth = uniform(depth_);
+        stride = uniform64(o.stride);
+        base = uniform(o.base + (KC ? first * o.stride : first * (size_t)EB));
+        high = uniform(o.rows - first);   // (KC) lines from the tile's first on
+        wide = uniform(o.cols - first);   // (otherwise) elements of a line from the tile's first on
+        const unsigned t = offset_here(threadIdx.x);   // (nothing of it is kept over the steps)
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            const bool in = KC ? line(q, t) < high : unit(q, t) * E < wide;
+            off[q] = in ? line(q, t) * (unsigned)stride + unit(q, t) * 16 : kOutside;
+        }
+    }
+    __device__ __forceinline__ void end() { depth = 0; }
+    // Where the step begins; the units that are not whole go outside.
+    __device__ __forceinline__ const char* at_step(unsigned k) {
+        step = k;
+        if (__builtin_expect(k + TILE::S >= depth, 0)) {   // (nor is a step after this one whole)
+            const unsigned t = offset_here(threadIdx.x);
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                const unsigned u = unit(q, t) * E, l = line(q, t);
+                const bool in = KC ? k + u + E <= depth
+                                   : k + l + 1 < depth || (k + l + 1 == depth && u + E <= wide);
+                off[q] = in ? off[q] : kOutside;
+            }
+        }
+        return base + (KC ? k * (size_t)EB : k * stride);
+    }
+    // Whether the step has cut units, whether this one is, and what it holds.
+    __device__ __forceinline__ bool cut() const {
+        if constexpr (KC) return step < depth && step + TILE::S > depth && depth % E;
+        else return step < depth && step + TILE::S >= depth && wide % E && wide < TILE::UNITS * E;
+    }
+    __device__ __forceinline__ bool cut(int q, unsigned t) const {
+        if constexpr (KC) return unit(q, t) == (depth - step) / E && line(q, t) < high;
+        else return unit(q, t) == wide / E && line(q, t) == depth - 1 - step;
+    }
+    __device__ __forceinline__ u32x4 rest(int q, unsigned t) const {
+        if constexpr (KC) return ld_end<EB>(base + line(q, t) * stride, depth, depth % E);
+        else return ld_end<EB>(base + (depth - 1) * stride, wide, wide % E);
+    }
+    // Writes the step's cut units over the zeros that this thread's loads left there.
+    __device__ __forceinline__ void mend(lds_t lds) const {
+        if (__builtin_expect(!cut(), 1)) return;
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);   // (loads straight into LDS, too)
+        const unsigned t = offset_here(threadIdx.x);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+            if (cut(q, t)) st_lds(slot(lds, q, t), rest(q, t));
+        // (known to the compiler, which would wait for these loads among the next step's:
+        // 64 experts of 1024 rows 1029 us, 906 so)
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+    }
+};
+
+// Through registers, for lines at any address.  A unit outside comes from a unit of
+// zeros, so that no load waits for a branch.
+__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
+
+template <int EB, class TILE, bool KC, int NT>
+struct Through : Lines<EB, TILE, KC, NT> {
+    using L = Lines<EB, TILE, KC, NT>;
+    u32x4 u[L::N];
+    const char* from;
+    __device__ __forceinline__ void aim(unsigned k) { from = this->at_step(k); }
     __device__ __forceinline__ void load(lds_t, int q) {
-        const int at = q * NT + (int)threadIdx.x;
-        const unsigned row = (KC ? first : k) + at / TILE::UNITS;
-        const unsigned col = (KC ? k : first) + at % TILE::UNITS * TILE::E;
-        u[q] = u32x4{0u, 0u, 0u, 0u};
-        if (row < o.rows) u[q] = ld_unit_of<EB>(o.base + row * o.stride, col, o.cols, 0u);
+        typedef const typename Vec<EB>::mem_t __attribute__((address_space(1))) * unit_t;
+        const unsigned f = this->off[q];
+        const uintptr_t zeros = (uintptr_t)&kZeros;
+        u[q] = *(unit_t)(f != L::kOutside ? (uintptr_t)from + f : zeros);
     }
     __device__ __forceinline__ void arrive(lds_t lds) const {
 #pragma unroll
-        for (int q = 0; q < N; ++q) {
-            const int at = q * NT + (int)threadIdx.x;
-            *(__attribute__((address_space(3))) u32x4*)(lds + TILE::at(at / TILE::UNITS,
-                                                                       at % TILE::UNITS)) = u[q];
-        }
+        for (int q = 0; q < L::N; ++q) st_lds(L::slot(lds, q, threadIdx.x), u[q]);
+        this->mend(lds);
     }
 };
 
 // (m0 is a register that the compiler keeps for itself: it sets it where it needs it)
 #pragma clang diagnostic ignored "-Winline-asm"
 
-// Straight into LDS, for lines of whole 16-byte units at 16-byte addresses whose
-// tile spans less than 2 GiB.  A wavefront's load fills 1 KiB of LDS in lane
-// order, so the swapping of units is in the addresses that the lanes read; a
-// unit outside the operand has an offset past the buffer and loads as zeros.
+// Straight into LDS, for lines at 4-byte addresses.  A wavefront's load fills 1 KiB of LDS in lane order, so the swapping of
+// units is in the addresses that the lanes read; an offset past the buffer loads
+// zeros.
 //
 // The load is written out because the compiler takes a transposing read for one
 // that may see the load's bytes, and waits for memory before it (the products of
 // 8192^3 by dout and by rows 1150 and 1130 us with the builtin, 773 and 816 so).
 // It has no register output, and meet() waits for it.
 template <int EB, class TILE, bool KC, int NT>
-struct Straight {
-    static constexpr int N = TILE::ROWS * TILE::UNITS / NT;
-    static_assert(TILE::ROWS * TILE::UNITS % NT == 0, "");
-    static constexpr unsigned kOutside = 0x80000000u;
-    const char* base;
-    unsigned off[N];
-    unsigned depth;
-    size_t stride;
+struct Straight : Lines<EB, TILE, KC, NT> {
+    using L = Lines<EB, TILE, KC, NT>;
     u32x4 buffer;
-    __device__ __forceinline__ static int line(int q, int thread) {
-        return (q * NT + thread) / TILE::UNITS;
-    }
-    __device__ __forceinline__ static int unit(int q, int thread) {   // in memory
-        return (q * NT + thread) % TILE::UNITS ^ TILE::swap_of(line(q, thread));
-    }
-    __device__ __forceinline__ void begin(const Operand& o, unsigned first, unsigned depth_) {
-        depth = depth_;
-        stride = o.stride;
-        base = o.base + (KC ? first * o.stride : first * (size_t)EB);
-        const int t = (int)offset_here(threadIdx.x);   // (nothing of it is kept over the steps)
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
-            const bool in = KC ? first + line(q, t) < o.rows : first + unit(q, t) * TILE::E < o.cols;
-            off[q] = in ? line(q, t) * (unsigned)o.stride + unit(q, t) * 16 : kOutside;
-        }
-    }
-    __device__ __forceinline__ void end() { depth = 0; }
     __device__ __forceinline__ void aim(unsigned k) {
-        const uint64_t at = (uint64_t)(uintptr_t)(base + (KC ? k * (size_t)EB : k * stride));
-        buffer = u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
-                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32)),
-                       0x7fffffffu, 0x00020000u};
-        if (k + TILE::S > depth) {   // (no step after this one is whole either)
-            const int t = (int)offset_here(threadIdx.x);
-#pragma unroll
-            for (int q = 0; q < N; ++q)
-                off[q] = k + (KC ? unit(q, t) * TILE::E : line(q, t)) < depth ? off[q] : kOutside;
-        }
+        const uint64_t at = uniform64((uint64_t)(uintptr_t)this->at_step(k));
+        buffer = u32x4{(uint32_t)at, (uint32_t)(at >> 32), 0x7fffffffu, 0x00020000u};
     }
     __device__ __forceinline__ void load(lds_t lds, int q) {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane(
-            (int)((uint32_t)(uintptr_t)lds + (q * NT + wave * 64) * 16));
+        const uint32_t at = uniform((uint32_t)(uintptr_t)L::slot(lds, q, threadIdx.x & ~63u));
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     :: "s"(at), "v"(off[q]), "s"(buffer) : "m0", "memory");
+                     :: "s"(at), "v"(this->off[q]), "s"(buffer) : "m0", "memory");
     }
-    __device__ __forceinline__ void arrive(lds_t) const {}
+    __device__ __forceinline__ void arrive(lds_t lds) const { this->mend(lds); }
 };
 
 // Everything this wavefront has asked for has arrived, then the block's
@@ -240,20 +313,58 @@ struct Job {
     unsigned i0, rows, j0, cols, depth;
 };
 
+// Takes part `p` of the job's depth where it is split, whole steps of `step`.
+template <int EB, bool AK, bool BK>
+__device__ __forceinline__ void take_part(Job* job, unsigned p, unsigned parts, unsigned step) {
+    const unsigned each = ((job->depth + step - 1) / step + parts - 1) / parts * step;
+    const unsigned from = p * each < job->depth ? p * each : job->depth;
+    const auto cut = [&](Operand& o, bool contiguous, unsigned to) {
+        o.base += contiguous ? from * (size_t)EB : from * o.stride;
+        (contiguous ? o.cols : o.rows) = to - from;
+    };
+    const unsigned to = job->depth - from < each ? job->depth : from + each;
+    cut(job->a, AK, to);
+    cut(job->b, BK, to);
+    job->depth = to - from;
+}
+
+// 4 elements of row i from column j on: of the result, or in 32 bits where it is
+// one of several parts.
+template <int EB>
+__device__ __forceinline__ void store(const Job& job, bool part, unsigned i, unsigned j, f32x4 v) {
+    const size_t at = (size_t)i * job.cols;
+    if (EB == 4 || part) st4<4>(job.c + at * 4, j, job.cols, v);
+    else st4<EB>(job.c + at * EB, j, job.cols, v);
+}
+
+// Two pieces side by side, as bf16: a lane has 4 neighbours of each, and the odd
+// rows of 16 lanes give theirs of the first piece for the even rows' of the
+// second, so that a lane has 8 neighbours of one row of one piece.
+__device__ __forceinline__ u32x4 pair(f32x4 a, f32x4 b) {
+    const f32x2_t v[4] = {{a[0], a[1]}, {a[2], a[3]}, {b[0], b[1]}, {b[2], b[3]}};
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        u[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v[i], bf16x2_t));
+    const auto x = __builtin_amdgcn_permlane16_swap(u[0], u[2], false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(u[1], u[3], false, false);
+    return u32x4{x[0], y[0], x[1], y[1]};
+}
+
 // Fills a tile with zeros.
 template <int EB, int TI, int TJ, int NT>
-__device__ __forceinline__ void clear(const Job& job) {
+__device__ __forceinline__ void clear(const Job& job, bool part) {
     const unsigned high = job.rows - job.i0 < TI ? job.rows - job.i0 : TI;
     for (unsigned at = threadIdx.x; at < high * (TJ / 4); at += NT)
-        st4<EB>(job.c + (size_t)(job.i0 + at / (TJ / 4)) * job.cols * EB, job.j0 + at % (TJ / 4) * 4, job.cols,
-                f32x4{0.f, 0.f, 0.f, 0.f});
+        store<EB>(job, part, job.i0 + at / (TJ / 4), job.j0 + at % (TJ / 4) * 4,
+                  f32x4{0.f, 0.f, 0.f, 0.f});
 }
 
 // A block's tiles one after another.  AK, BK: the reduced dimension is the
 // operand's contiguous one; AS, BS: its lines are for Straight.  JOBS::next gives
 // the next job, if there is one.
 //
-// LDS holds two steps.  A step has four parts, two of its depth by two of the
+// LDS holds two steps.  A step has parts, 64 bytes of its depth by half of the
 // wavefront's rows: while one part's pieces are multiplied, the next part's come
 // from LDS, one read after each matrix instruction, and before the last part the
 // wavefronts meet.  What they wait for there was asked for a whole step ago, and
@@ -261,11 +372,12 @@ __device__ __forceinline__ void clear(const Job& job) {
 // next go between the last part's instructions.  The tiles follow one another in
 // this without a gap: a tile's last two steps load the first two of the next,
 // and its result is stored while these come.
-template <int EB, bool AK, bool BK, bool AS, bool BS, int TI, int TJ, int WI, int WJ>
+template <int EB, bool AK, bool BK, bool AS, bool BS, int TI, int TJ, int WI, int WJ,
+          int STEP>
 struct Block {
     static constexpr int NT = WI * WJ * 64;
-    using A = Tile<EB, AK, TI>;
-    using B = Tile<EB, BK, TJ>;
+    using A = Tile<EB, AK, TI, STEP>;
+    using B = Tile<EB, BK, TJ, STEP>;
     using FeedA = std::conditional_t<AS, Straight<EB, A, AK, NT>, Through<EB, A, AK, NT>>;
     using FeedB = std::conditional_t<BS, Straight<EB, B, BK, NT>, Through<EB, B, BK, NT>>;
     static constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;   // a wavefront's 16 x 16 pieces
@@ -282,22 +394,23 @@ struct Block {
         FeedA feed_a;
         FeedB feed_b;
         f32x4 acc[FI][FJ];
-        Piece a0[H], a1[H], b0[FJ], b1[FJ];
+        Piece pa[2][H], pb[2][FJ];
         const unsigned from_a = A::origin(lane, wi), from_b = A::BYTES + B::origin(lane, wj);
-        const auto read_a = [&](Piece (&p)[H], lds_t at, int s, int half, int i) {
-            p[i] = A::frag(at + from_a, 16 * WI * (half * H + i), s);
+        // Part p: rows' half p % 2 of the depth's part p / 2.  Read r of those that it needs.
+        const auto read = [&](lds_t at, int p, int r) {
+            if (r < H) pa[p & 1][r] = A::frag(at + from_a, 16 * WI * (p % 2 * H + r), p / 2);
+            else if (p % 2 == 0 && r < H + FJ)
+                pb[p / 2 & 1][r - H] = B::frag(at + from_b, 16 * (r - H), p / 2);
         };
-        const auto read_b = [&](Piece (&p)[FJ], lds_t at, int s, int j) {
-            p[j] = B::frag(at + from_b, 16 * j, s);
-        };
-        const auto multiply = [&](const Piece (&pa)[H], const Piece (&pb)[FJ], int half, auto also) {
+        const auto multiply = [&](int p, auto also) {
             __builtin_amdgcn_sched_barrier(0);
             // (the operands change places, so that a lane holds 4 neighbours of a row)
 #pragma unroll
             for (int i = 0; i < H; ++i)
 #pragma unroll
                 for (int j = 0; j < FJ; ++j) {
-                    acc[half * H + i][j] = mma(pb[j], pa[i], acc[half * H + i][j]);
+                    f32x4& c = acc[p % 2 * H + i][j];
+                    c = mma(pb[p / 2 & 1][j], pa[p & 1][i], c);
                     also(i * FJ + j);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -319,6 +432,8 @@ struct Block {
             feed_b.arrive(at + A::BYTES);
         };
         constexpr int LOADS = FeedA::N + FeedB::N, READS = H + FJ, SLOTS = H * FJ;
+        constexpr int PARTS = 2 * STEP / 64;
+        static_assert(PARTS % 4 == 0, "a step ends with the registers that it began with");
         Job job, after;
         if (!jobs.next(&job)) return;
         begin(job);
@@ -328,8 +443,8 @@ struct Block {
         meet();
         aim(A::S);
         for (int q = 0; q < LOADS; ++q) load(lds + STAGE, q);
-        for (int i = 0; i < H; ++i) read_a(a0, lds, 0, 0, i);
-        for (int j = 0; j < FJ; ++j) read_b(b0, lds, 0, j);
+#pragma unroll
+        for (int r = 0; r < READS; ++r) read(lds, 0, r);
         int at = 0;
         for (bool more = true; more;) {
 #pragma unroll
@@ -337,23 +452,22 @@ struct Block {
 #pragma unroll
                 for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
             // (two steps at least, so that the loads are never more than one tile ahead)
-            unsigned left = (job.depth + A::S - 1) / A::S, ahead = 2 * A::S;
+            unsigned left = uniform((job.depth + A::S - 1) / A::S), ahead = 2 * A::S;
             left = left < 2 ? 2 : left;
             for (; left; --left) {
                 const lds_t now = lds + at, next = lds + (at ^= STAGE);
-                multiply(a0, b0, 0, [&](int n) {
-                    if (n < H) read_a(a1, now, 0, 1, n);
-                });
-                multiply(a1, b0, 1, [&](int n) {
-                    if (n < H) read_a(a0, now, 1, 0, n);
-                    else if (n < READS) read_b(b1, now, 1, n - H);
-                });
-                multiply(a0, b1, 0, [&](int n) {
-                    if (n < H) read_a(a1, now, 1, 1, n);
-                });
+#pragma unroll
+                for (int p = 0; p < PARTS - 1; ++p)
+                    multiply(p, [&](int i) {   // (in the part's first half)
+                        constexpr int HALF = SLOTS > 1 ? SLOTS / 2 : 1;
+                        if (i < HALF)
+#pragma unroll
+                            for (int r = i * READS / HALF; r < (i + 1) * READS / HALF; ++r)
+                                read(now, p + 1, r);
+                    });
                 arrive(next);
                 meet();
-                if (left == 2) {
+                if (__builtin_expect(left == 2, 0)) {
                     more = jobs.next(&after);
                     ahead = 0;
                     if (more) {
@@ -365,25 +479,34 @@ struct Block {
                 }
                 aim(ahead);
                 ahead += A::S;
-                multiply(a1, b1, 1, [&](int n) {
-                    // READS reads and LOADS loads over the part's SLOTS instructions
+                multiply(PARTS - 1, [&](int i) {
 #pragma unroll
-                    for (int r = n * READS / SLOTS; r < (n + 1) * READS / SLOTS; ++r) {
-                        if (r < H) read_a(a0, next, 0, 0, r);
-                        else read_b(b0, next, 0, r - H);
-                    }
+                    for (int r = i * READS / SLOTS; r < (i + 1) * READS / SLOTS; ++r) read(next, 0, r);
 #pragma unroll
-                    for (int q = n * LOADS / SLOTS; q < (n + 1) * LOADS / SLOTS; ++q) load(now, q);
+                    for (int q = i * LOADS / SLOTS; q < (i + 1) * LOADS / SLOTS; ++q) load(now, q);
                 });
             }
+            const bool part = jobs.a.parts > 1;
 #pragma unroll
             for (int i = 0; i < FI; ++i) {
                 const unsigned row = job.i0 + wi + 16 * WI * i + (lane & 15);
+                const unsigned col = job.j0 + wj;
+                if constexpr (EB == 2 && FJ % 2 == 0) {
+                    if (__builtin_expect(!part, 1)) {
+#pragma unroll
+                        for (int j = 0; j < FJ; j += 2) {
+                            const u32x4 u = pair(acc[i][j], acc[i][j + 1]);
+                            const unsigned at = col + 16 * j + 16 * (lane >> 4 & 1) + 8 * (lane >> 5);
+                            if (row < job.rows)
+                                st_unit_of<2>(job.c + (size_t)row * job.cols * 2, at, job.cols, u);
+                        }
+                        continue;
+                    }
+                }
                 if (row < job.rows)
 #pragma unroll
                     for (int j = 0; j < FJ; ++j)
-                        st4<EB>(job.c + (size_t)row * job.cols * EB, job.j0 + wj + 16 * j + 4 * (lane >> 4),
-                                job.cols, acc[i][j]);
+                        store<EB>(job, part, row, col + 16 * j + 4 * (lane >> 4), acc[i][j]);
             }
             job = after;
         }
@@ -410,29 +533,27 @@ __device__ __forceinline__ void patch(unsigned at, unsigned down, unsigned acros
     *j = rest / high;
 }
 
-// The groups of rows: expert e has [begin[e], end[e]), whatever the offsets hold
-// inside [0, nrows]; group `experts` is the rows behind the last expert.  tiles[e]
+// The groups of rows: expert e has [begin[e], end(e)), whatever the offsets hold
+// inside [0, nrows] and with the first row in group 0; group `experts` is the rows behind the last expert.  tiles[e]
 // are those of the groups up to e, each group beginning a tile of its own.
 constexpr int kGroups = 1024 + 1;
 struct Groups {
-    int begin[kGroups], end[kGroups], tiles[kGroups];
+    int begin[kGroups + 1], tiles[kGroups];
+    __device__ __forceinline__ int end(int e) const { return max(begin[e], begin[e + 1]); }
     // (called by the whole block; `height` rows a tile)
     __device__ __forceinline__ void fill(const ProductArgs& a, int height) {
-        const int lane = threadIdx.x & 63, n = (int)a.nrows;
-        if (threadIdx.x < 64) {
+        const int n = (int)a.nrows;
+        for (int e = threadIdx.x; e <= a.experts + 1; e += blockDim.x) {
+            const int o = e == 0 ? 0 : e <= a.experts ? a.offsets[e] : n;
+            begin[e] = o < 0 ? 0 : o < n ? o : n;
+        }
+        __syncthreads();
+        const int lane = threadIdx.x;
+        if (lane < 64) {
             int run = 0;
             for (int e0 = 0; e0 <= a.experts; e0 += 64) {
-                const int e = e0 + lane;
-                int b = 0, f = 0;
-                if (e <= a.experts) {
-                    b = a.offsets[e];
-                    f = e < a.experts ? a.offsets[e + 1] : n;
-                    b = b < 0 ? 0 : b < n ? b : n;
-                    f = f < b ? b : f < n ? f : n;
-                    begin[e] = b;
-                    end[e] = f;
-                }
-                int inc = (f - b) / height + ((f - b) % height ? 1 : 0);
+                const int e = e0 + lane, rows = e <= a.experts ? end(e) - begin[e] : 0;
+                int inc = rows / height + (rows % height ? 1 : 0);
 #pragma unroll
                 for (int d = 1; d < 64; d <<= 1) {
                     const int o = __shfl_up(inc, d, 64);
@@ -455,16 +576,23 @@ struct Groups {
     }
 };
 
+// The arguments, and how many parts the reduced dimension has: more than one
+// leave sums in 32 bits to `work`, one result after the other.
+struct PartArgs : ProductArgs {
+    unsigned parts;
+};
+
 // The tiles of the rows' products (KIND: forward or drows) that this block has.
-template <int EB, ProductKind KIND, int TI, int TJ, int NT>
+template <int EB, ProductKind KIND, int TI, int TJ, int NT, int STEP>
 struct RowJobs {
-    const ProductArgs& a;
+    const PartArgs& a;
     const Groups& groups;
-    unsigned id, across, total;
-    __device__ __forceinline__ RowJobs(const ProductArgs& args, const Groups& g)
+    unsigned id, across, tiles, total;
+    __device__ __forceinline__ RowJobs(const PartArgs& args, const Groups& g)
         : a(args), groups(g), id(blockIdx.x) {
         across = (cols() + TJ - 1) / TJ;
-        total = across * down();
+        tiles = across * down();
+        total = tiles * a.parts;
     }
     __device__ __forceinline__ unsigned cols() const {
         return (unsigned)(KIND == PRODUCT_FORWARD ? a.out : a.hidden);
@@ -476,26 +604,29 @@ struct RowJobs {
         for (; id / kDies <= total / kDies; id += gridDim.x) {
             const int at = tile_of(id, total);
             if (at < 0) continue;
+            const unsigned p = (unsigned)at / tiles;
             unsigned ti, tj;
-            patch((unsigned)at, down(), across, &ti, &tj);
+            patch((unsigned)at - p * tiles, down(), across, &ti, &tj);
             const int e = groups.of((int)ti, a.experts);
             const int begin = __builtin_amdgcn_readfirstlane(groups.begin[e]);
-            const int end = __builtin_amdgcn_readfirstlane(groups.end[e]);
+            const int end = __builtin_amdgcn_readfirstlane(groups.end(e));
             const int before = e ? __builtin_amdgcn_readfirstlane(groups.tiles[e - 1]) : 0;
             const unsigned depth = (unsigned)(KIND == PRODUCT_FORWARD ? a.hidden : a.out);
             job->a = {static_cast<const char*>(a.a), a.astride * EB, (unsigned)end, depth};
-            job->c = static_cast<char*>(a.c);
+            job->c = a.parts == 1 ? static_cast<char*>(a.c)
+                                  : reinterpret_cast<char*>(a.work + p * a.nrows * cols());
             job->i0 = (unsigned)begin + (ti - before) * TI;
             job->rows = (unsigned)end;
             job->j0 = tj * TJ;
             job->cols = cols();
             job->depth = depth;
-            if (e == a.experts) {
-                clear<EB, TI, TJ, NT>(*job);
+            job->b = {static_cast<const char*>(a.b) + (e < a.experts ? (size_t)e : 0) * a.out * a.hidden * EB,
+                      a.hidden * EB, (unsigned)a.out, (unsigned)a.hidden};
+            if (a.parts > 1) take_part<EB, true, KIND == PRODUCT_FORWARD>(job, p, a.parts, STEP / EB);
+            if (e == a.experts || job->depth == 0) {
+                clear<EB, TI, TJ, NT>(*job, a.parts > 1);
                 continue;
             }
-            job->b = {static_cast<const char*>(a.b) + (size_t)e * a.out * a.hidden * EB,
-                      a.hidden * EB, (unsigned)a.out, (unsigned)a.hidden};
             id += gridDim.x;
             return true;
         }
@@ -504,39 +635,44 @@ struct RowJobs {
 };
 
 // The tiles of the weights' gradient.
-template <int EB, int TI, int TJ, int NT>
+template <int EB, int TI, int TJ, int NT, int STEP>
 struct WeightJobs {
-    const ProductArgs& a;
+    const PartArgs& a;
     const Groups& groups;
-    unsigned id, across, down, total;
-    __device__ __forceinline__ WeightJobs(const ProductArgs& args, const Groups& g)
+    unsigned id, across, down, tiles, total;
+    __device__ __forceinline__ WeightJobs(const PartArgs& args, const Groups& g)
         : a(args), groups(g), id(blockIdx.x) {
         across = (unsigned)((a.hidden + TJ - 1) / TJ);
         down = (unsigned)((a.out + TI - 1) / TI);
-        total = across * down * (unsigned)a.experts;
+        tiles = across * down * (unsigned)a.experts;
+        total = tiles * a.parts;
     }
     __device__ __forceinline__ bool next(Job* job) {
         for (; id / kDies <= total / kDies; id += gridDim.x) {
             const int at = tile_of(id, total);
             if (at < 0) continue;
-            const unsigned e = (unsigned)at / (across * down);
+            const unsigned p = (unsigned)at / tiles, t = (unsigned)at - p * tiles;
+            const unsigned e = t / (across * down);
             unsigned ti, tj;
-            patch((unsigned)at - e * across * down, down, across, &ti, &tj);
+            patch(t - e * across * down, down, across, &ti, &tj);
             const int begin = __builtin_amdgcn_readfirstlane(groups.begin[e]);
-            const int end = __builtin_amdgcn_readfirstlane(groups.end[e]);
+            const int end = __builtin_amdgcn_readfirstlane(groups.end(e));
             const unsigned n = (unsigned)(end - begin);
             job->a = {static_cast<const char*>(a.a) + (size_t)begin * a.astride * EB,
                       a.astride * EB, n, (unsigned)a.out};
             job->b = {static_cast<const char*>(a.b) + (size_t)begin * a.bstride * EB,
                       a.bstride * EB, n, (unsigned)a.hidden};
-            job->c = static_cast<char*>(a.c) + (size_t)e * a.out * a.hidden * EB;
+            const size_t each = a.out * a.hidden;
+            job->c = a.parts == 1 ? static_cast<char*>(a.c) + e * each * EB
+                                  : reinterpret_cast<char*>(a.work + (p * a.experts + e) * each);
             job->i0 = ti * TI;
             job->rows = (unsigned)a.out;
             job->j0 = tj * TJ;
             job->cols = (unsigned)a.hidden;
             job->depth = n;
-            if (n == 0) {
-                clear<EB, TI, TJ, NT>(*job);
+            if (a.parts > 1) take_part<EB, false, false>(job, p, a.parts, STEP / EB);
+            if (job->depth == 0) {
+                clear<EB, TI, TJ, NT>(*job, a.parts > 1);
                 continue;
             }
             id += gridDim.x;
@@ -546,19 +682,52 @@ struct WeightJobs {
     }
 };
 
-template <int EB, ProductKind KIND, bool AS, bool BS, int TI, int TJ, int WI, int WJ>
-__global__ __launch_bounds__(WI * WJ * 64, 2) void k_product(const ProductArgs a) {
-    constexpr int NT = WI * WJ * 64;
-    using BLOCK = Block<EB, KIND != PRODUCT_DWEIGHTS, KIND == PRODUCT_FORWARD, AS, BS, TI, TJ, WI, WJ>;
+// The shapes of a block's tile: TI x TJ, WI x WJ wavefronts, steps of STEP bytes,
+// EACH blocks a compute unit.
+template <int TI_, int TJ_, int WI_, int WJ_, int STEP_, int EACH_>
+struct Shape {
+    static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, STEP = STEP_, EACH = EACH_;
+    static constexpr int NT = WI * WJ * 64;
+};
+using Large = Shape<256, 256, 2, 4, 128, 1>;
+using Middle = Shape<128, 128, 2, 2, 128, 2>;
+using Small = Shape<32, 64, 1, 4, 256, 2>;
+
+template <int EB, ProductKind KIND, bool AS, bool BS, class SHAPE>
+__global__ __launch_bounds__(SHAPE::NT, SHAPE::EACH * SHAPE::NT / 256) void k_product(
+    const PartArgs a) {
+    using BLOCK = Block<EB, KIND != PRODUCT_DWEIGHTS, KIND == PRODUCT_FORWARD, AS, BS, SHAPE::TI,
+                        SHAPE::TJ, SHAPE::WI, SHAPE::WJ, SHAPE::STEP>;
     __shared__ __attribute__((aligned(1024))) char lds[2 * BLOCK::STAGE];
     __shared__ Groups groups;
-    groups.fill(a, TI);
+    groups.fill(a, SHAPE::TI);
     if constexpr (KIND == PRODUCT_DWEIGHTS) {
-        WeightJobs<EB, TI, TJ, NT> jobs(a, groups);
+        WeightJobs<EB, SHAPE::TI, SHAPE::TJ, SHAPE::NT, SHAPE::STEP> jobs(a, groups);
         BLOCK::run((lds_t)lds, jobs);
     } else {
-        RowJobs<EB, KIND, TI, TJ, NT> jobs(a, groups);
+        RowJobs<EB, KIND, SHAPE::TI, SHAPE::TJ, SHAPE::NT, SHAPE::STEP> jobs(a, groups);
         BLOCK::run((lds_t)lds, jobs);
+    }
+}
+
+// The sum of the parts, each n elements.
+template <int EB>
+__global__ __launch_bounds__(256) void k_product_join(const float* part, unsigned parts, size_t n,
+                                                      char* c) {
+    constexpr int E = Vec<EB>::E;
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * E; i < n;
+         i += (size_t)gridDim.x * 256 * E) {
+        float sum[E] = {};
+        for (unsigned p = 0; p < parts; ++p) {
+            const char* from = reinterpret_cast<const char*>(part + p * n);
+#pragma unroll
+            for (int h = 0; h < E / 4; ++h) {
+                const u32x4 u = ld_unit_of<4>(from, i + 4 * h, n, 0u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[4 * h + j] += as_f32(u[j]);
+            }
+        }
+        st_unit_of<EB>(c, i, n, Vec<EB>::pack(sum));
     }
 }
 
@@ -575,42 +744,119 @@ unsigned blocks_of(size_t tiles, size_t each) {
     return (unsigned)(b < kUnits * each ? b : kUnits * each);
 }
 
-// Whether lines of n elements, `stride` elements apart from p on, are whole
-// 16-byte units, and 512 of them span less than 2 GiB.
-bool lines(const void* p, size_t n, size_t stride, int eb) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && n * eb % 16 == 0 && stride * eb % 16 == 0 &&
-           stride * eb < (size_t(1) << 22);
+template <int EB, ProductKind KIND, bool AS, bool BS, class SHAPE>
+hipError_t launch(const PartArgs& a, hipStream_t s) {
+    const size_t cols = KIND == PRODUCT_FORWARD ? a.out : a.hidden;
+    const size_t high = KIND == PRODUCT_DWEIGHTS
+                            ? (a.out + SHAPE::TI - 1) / SHAPE::TI * a.experts
+                            : most_row_tiles(a.nrows, a.experts, SHAPE::TI);
+    const size_t tiles = high * ((cols + SHAPE::TJ - 1) / SHAPE::TJ) * a.parts;
+    if (tiles > size_t(INT_MAX) - 64 * kUnits) return hipErrorInvalidValue;   // (no memory holds them)
+    hipLaunchKernelGGL((k_product<EB, KIND, AS, BS, SHAPE>), dim3(blocks_of(tiles, SHAPE::EACH)),
+                       dim3(SHAPE::NT), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1) return e;
+    const size_t n = (KIND == PRODUCT_DWEIGHTS ? a.out * a.experts : a.nrows) * cols;
+    const size_t blocks = (n + 256 * (16 / EB) - 1) / (256 * (16 / EB));
+    hipLaunchKernelGGL(k_product_join<EB>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0,
+                       s, a.work, a.parts, n, static_cast<char*>(a.c));
+    return hipGetLastError();
 }
 
-template <int EB, ProductKind KIND, bool AS, bool BS, int T, int WI, int WJ>
-hipError_t launch(const ProductArgs& a, hipStream_t s) {
-    const size_t cols = KIND == PRODUCT_FORWARD ? a.out : a.hidden;
-    const size_t high = KIND == PRODUCT_DWEIGHTS ? (a.out + T - 1) / T * a.experts
-                                                 : most_row_tiles(a.nrows, a.experts, T);
-    const size_t tiles = high * ((cols + T - 1) / T);
-    if (tiles > size_t(INT_MAX) - 64 * kUnits) return hipErrorInvalidValue;   // (no memory holds them)
-    const unsigned blocks = blocks_of(tiles, T == 256 ? 1 : 2);
-    hipLaunchKernelGGL((k_product<EB, KIND, AS, BS, T, T, WI, WJ>), dim3(blocks), dim3(WI * WJ * 64),
-                       0, s, a);
-    return hipGetLastError();
+// Lines of fp32 are always for Straight; those of bf16 where they are an even
+// number of elements apart, at 4-byte addresses.
+template <int EB, ProductKind KIND, class SHAPE>
+hipError_t by_lines(const PartArgs& a, hipStream_t s) {
+    if constexpr (EB == 4) return launch<EB, KIND, true, true, SHAPE>(a, s);
+    else {
+        const auto even = [](const void* p, size_t stride) {
+            return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
+        };
+        const bool as = even(a.a, a.astride);
+        const bool bs = even(a.b, KIND == PRODUCT_DWEIGHTS ? a.bstride : a.hidden);
+        if (as && bs) return launch<EB, KIND, true, true, SHAPE>(a, s);
+        if constexpr (SHAPE::TI == 256) return by_lines<EB, KIND, Middle>(a, s);
+        else if (as) return launch<EB, KIND, true, false, SHAPE>(a, s);
+        else if (bs) return launch<EB, KIND, false, true, SHAPE>(a, s);
+        else return launch<EB, KIND, false, false, SHAPE>(a, s);
+    }
+}
+
+// How a product is computed: the tile's shape and the parts of its depth, from the
+// time that each would take.  A block's tile takes `each` us and `step` us for a
+// step; `alone` where a compute unit has one block.
+struct Cost {
+    int ti, tj, step_bytes, blocks;
+    double each, step, alone;
+};
+// (measured on MI355X; see the table at the top)
+constexpr Cost kCosts[2][2][3] = {
+    // bf16, lines for Straight; and through registers
+    {{{256, 256, 128, 1, 6.0, 1.4, 1.4}, {128, 128, 128, 2, 4.0, 1.0, 0.62}, {32, 64, 256, 2, 3.5, 0.62, 0.6}},
+     {{256, 256, 128, 1, 6.0, 9.0, 9.0}, {128, 128, 128, 2, 4.0, 1.5, 1.0}, {32, 64, 256, 2, 3.5, 1.0, 0.9}}},
+    // fp32
+    {{{256, 256, 128, 1, 6.0, 99.0, 99.0}, {128, 128, 128, 2, 4.0, 3.7, 1.95}, {32, 64, 256, 2, 3.5, 1.13, 0.7}},
+     {{256, 256, 128, 1, 6.0, 99.0, 99.0}, {128, 128, 128, 2, 4.0, 3.7, 1.95}, {32, 64, 256, 2, 3.5, 1.13, 0.7}}}};
+
+struct Plan {
+    int shape;
+    unsigned parts;
+};
+
+Plan plan_of(ProductKind kind, size_t nrows, int experts, size_t hidden, size_t out, int eb) {
+    // (rows are taken as spread evenly over the experts that can have some)
+    const size_t used = nrows < (size_t)experts ? (nrows ? nrows : 1) : (size_t)experts;
+    const size_t rows = (nrows + used - 1) / used;
+    const size_t cols = kind == PRODUCT_FORWARD ? out : hidden;
+    const size_t depth = kind == PRODUCT_FORWARD ? hidden : kind == PRODUCT_DROWS ? out : rows;
+    const size_t results = kind == PRODUCT_DWEIGHTS ? (size_t)experts * out * hidden : nrows * cols;
+    const bool odd = eb == 2 && (hidden % 2 || (kind != PRODUCT_FORWARD && out % 2));
+    Plan best{1, 1};
+    double least = 1e300;
+    for (int i = 0; i < 3; ++i) {
+        const Cost& c = kCosts[eb == 4][odd][i];
+        const size_t down = kind == PRODUCT_DWEIGHTS ? (out + c.ti - 1) / c.ti * (size_t)experts
+                                                     : (rows + c.ti - 1) / c.ti * used;
+        const double tiles = (double)down * ((cols + c.tj - 1) / c.tj);
+        const size_t steps = (depth * eb + c.step_bytes - 1) / c.step_bytes;
+        for (unsigned parts = 1; parts <= 16; parts *= 2) {
+            if (parts > 1 && steps < 4 * parts) break;
+            const size_t n = (steps + parts - 1) / parts;
+            const double all = tiles * parts;
+            const double rounds = std::ceil(all / (kUnits * c.blocks));
+            double t = rounds * (c.each + (n < 2 ? 2 : n) * (all <= kUnits ? c.alone : c.step));
+            // (a launch, and the parts' traffic at 4 TB/s)
+            if (parts > 1) t += 4.0 + results * (8.0 * parts) / 4e6;
+            if (t < least * 0.97) {
+                least = t;
+                best = {i, parts};
+            }
+        }
+    }
+    return best;
 }
 
 template <int EB, ProductKind KIND>
 hipError_t launch(const ProductArgs& a, hipStream_t s) {
-    const size_t acols = KIND == PRODUCT_FORWARD ? a.hidden : a.out;
-    const bool as = lines(a.a, acols, a.nrows > 1 ? a.astride : acols, a.eb);
-    const bool bs = lines(a.b, a.hidden,
-                          KIND == PRODUCT_DWEIGHTS && a.nrows > 1 ? a.bstride : a.hidden, a.eb);
-    if (as && bs) {
-        if constexpr (EB == 2) return launch<EB, KIND, true, true, 256, 2, 4>(a, s);
-        else return launch<EB, KIND, true, true, 128, 2, 2>(a, s);
-    }
-    return launch<EB, KIND, false, false, 128, 2, 2>(a, s);
+    const Plan plan = plan_of(KIND, a.nrows, a.experts, a.hidden, a.out, EB);
+    PartArgs p;
+    static_cast<ProductArgs&>(p) = a;
+    p.parts = plan.parts;
+    if (plan.shape == 2) return by_lines<EB, KIND, Small>(p, s);
+    if constexpr (EB == 2)
+        if (plan.shape == 0) return by_lines<EB, KIND, Large>(p, s);
+    return by_lines<EB, KIND, Middle>(p, s);
 }
 
 }  // namespace
 
-size_t product_work_bytes(ProductKind, size_t, int, size_t, size_t, int) { return 0; }
+size_t product_work_bytes(ProductKind kind, size_t nrows, int experts, size_t hidden, size_t out,
+                          int eb) {
+    const unsigned parts = plan_of(kind, nrows, experts, hidden, out, eb).parts;
+    if (parts == 1) return 0;
+    const size_t rows = kind == PRODUCT_DWEIGHTS ? out * (size_t)experts : nrows;
+    return rows * (kind == PRODUCT_FORWARD ? out : hidden) * parts * sizeof(float);
+}
 
 hipError_t launch_product(ProductKind kind, const ProductArgs& a, hipStream_t s) {
     if (kind == PRODUCT_DWEIGHTS)

@@ -53,9 +53,9 @@ def embedding_backward(dy, ids, vocab, scale):
 # ---------------------------------------------------------------- the experts' products
 
 def groups(offsets, n):
-    """The experts' rows, from offsets as they may come: inside [0, n], none where
-    the end lies before the beginning."""
-    o = [min(max(int(v), 0), n) for v in offsets.tolist()]
+    """The experts' rows, from offsets as they may come: inside [0, n], the first 0,
+    none where the end lies before the beginning."""
+    o = [0, *(min(max(int(v), 0), n) for v in offsets.tolist()[1:])]
     return [(b, max(b, e)) for b, e in zip(o[:-1], o[1:])]
 
 
