@@ -146,7 +146,9 @@ constexpr int kVmcnt0 = 0x0f70;
 //
 // A unit outside the operand is zeros.  So is one that a line's end cuts, where
 // what lies behind it may not be read (behind the reduced dimension, and behind
-// the operand's last line), but for the elements that belong to it.
+// the operand's last line), but for the elements that belong to it.  Lines closer
+// together than a unit (`narrow`) are cut every one: a unit would reach over
+// several of them, and over the last from lines before it.
 template <int EB, class TILE, bool KC, int NT>
 struct Lines {
     static constexpr int N = TILE::ROWS * TILE::UNITS / NT;
@@ -157,6 +159,7 @@ struct Lines {
     unsigned off[N];        // bytes from the step's begin
     unsigned depth, wide, high, step;
     size_t stride;
+    bool narrow;
     // Thread t's unit q, which goes to LDS unit q * NT + t: its line, and its unit in memory.
     __device__ __forceinline__ static unsigned line(int q, unsigned t) {
         return ((unsigned)(q * NT) + t) / TILE::UNITS;
@@ -170,13 +173,14 @@ struct Lines {
     __device__ __forceinline__ void begin(const Operand& o, unsigned first, unsigned depth_) {
         depth = uniform(depth_);
         stride = uniform64(o.stride);
+        narrow = !KC && stride < 16;
         base = uniform(o.base + (KC ? first * o.stride : first * (size_t)EB));
         high = uniform(o.rows - first);   // (KC) lines from the tile's first on
         wide = uniform(o.cols - first);   // (otherwise) elements of a line from the tile's first on
         const unsigned t = offset_here(threadIdx.x);   // (nothing of it is kept over the steps)
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-            const bool in = KC ? line(q, t) < high : unit(q, t) * E < wide;
+            const bool in = KC ? line(q, t) < high : unit(q, t) * E < wide && !narrow;
             off[q] = in ? line(q, t) * (unsigned)stride + unit(q, t) * 16 : kOutside;
         }
     }
@@ -199,15 +203,17 @@ struct Lines {
     // Whether the step has cut units, whether this one is, and what it holds.
     __device__ __forceinline__ bool cut() const {
         if constexpr (KC) return step < depth && step + TILE::S > depth && depth % E;
-        else return step < depth && step + TILE::S >= depth && wide % E && wide < TILE::UNITS * E;
+        else return step < depth && (narrow || (step + TILE::S >= depth && wide % E &&
+                                                wide < TILE::UNITS * E));
     }
     __device__ __forceinline__ bool cut(int q, unsigned t) const {
         if constexpr (KC) return unit(q, t) == (depth - step) / E && line(q, t) < high;
-        else return unit(q, t) == wide / E && line(q, t) == depth - 1 - step;
+        else return narrow ? unit(q, t) == 0 && line(q, t) < depth - step
+                           : unit(q, t) == wide / E && line(q, t) == depth - 1 - step;
     }
     __device__ __forceinline__ u32x4 rest(int q, unsigned t) const {
         if constexpr (KC) return ld_end<EB>(base + line(q, t) * stride, depth, depth % E);
-        else return ld_end<EB>(base + (depth - 1) * stride, wide, wide % E);
+        else return ld_end<EB>(base + (step + line(q, t)) * stride, wide, wide % E);
     }
     // Writes the step's cut units over the zeros that this thread's loads left there.
     __device__ __forceinline__ void mend(lds_t lds) const {

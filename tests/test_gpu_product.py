@@ -66,6 +66,14 @@ def test_widths(hidden, out, t):
     check((40, 150, 9), hidden, out, t, 2)
 
 
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("hidden,out", [(1, 200), (2, 1), (3, 70), (4, 9), (5, 5), (6, 31), (7, 2),
+                                        (8, 7), (9, 3), (70, 3), (200, 7)])
+def test_narrow(hidden, out, t):
+    """Lines closer together than 16 bytes, over several steps of the depth."""
+    check((200, 0, 131, 1), hidden, out, t, 2)
+
+
 def test_large():
     """Tiles of every kind among many rows."""
     check((3000, 100, 0, 2500, 260, 1), 1024, 1280, BF, 30)
