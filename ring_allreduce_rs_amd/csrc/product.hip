@@ -317,6 +317,7 @@ struct Job {
     Operand a, b;
     char* c;
     unsigned i0, rows, j0, cols, depth;
+    unsigned turn;      // the step that comes first; those before it come last
 };
 
 // Takes part `p` of the job's depth where it is split, whole steps of `step`.
@@ -440,14 +441,31 @@ struct Block {
         constexpr int LOADS = FeedA::N + FeedB::N, READS = H + FJ, SLOTS = H * FJ;
         constexpr int PARTS = 2 * STEP / 64;
         static_assert(PARTS % 4 == 0, "a step ends with the registers that it began with");
+        // The step that is loaded next, and where to begin anew for the steps before `turn`.
+        constexpr unsigned kNever = ~0u;
+        unsigned ahead, again;
+        const auto start = [&](const Job& job) {
+            begin(job);
+            ahead = job.turn * A::S;
+            again = job.turn ? job.depth : kNever;
+        };
+        const auto advance = [&](const Job& job) {
+            if (__builtin_expect(ahead >= again, 0)) {
+                begin(job);
+                ahead = 0;
+                again = kNever;
+            }
+            aim(ahead);
+            ahead += A::S;
+        };
         Job job, after;
         if (!jobs.next(&job)) return;
-        begin(job);
-        aim(0);
+        start(job);
+        advance(job);
         for (int q = 0; q < LOADS; ++q) load(lds, q);
         arrive(lds);
         meet();
-        aim(A::S);
+        advance(job);
         for (int q = 0; q < LOADS; ++q) load(lds + STAGE, q);
 #pragma unroll
         for (int r = 0; r < READS; ++r) read(lds, 0, r);
@@ -458,7 +476,7 @@ struct Block {
 #pragma unroll
                 for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
             // (two steps at least, so that the loads are never more than one tile ahead)
-            unsigned left = uniform((job.depth + A::S - 1) / A::S), ahead = 2 * A::S;
+            unsigned left = uniform((job.depth + A::S - 1) / A::S);
             left = left < 2 ? 2 : left;
             for (; left; --left) {
                 const lds_t now = lds + at, next = lds + (at ^= STAGE);
@@ -475,16 +493,16 @@ struct Block {
                 meet();
                 if (__builtin_expect(left == 2, 0)) {
                     more = jobs.next(&after);
-                    ahead = 0;
                     if (more) {
-                        begin(after);
+                        start(after);
                     } else {
                         feed_a.end();
                         feed_b.end();
+                        ahead = 0;
+                        again = kNever;
                     }
                 }
-                aim(ahead);
-                ahead += A::S;
+                advance(left > 2 ? job : after);
                 multiply(PARTS - 1, [&](int i) {
 #pragma unroll
                     for (int r = i * READS / SLOTS; r < (i + 1) * READS / SLOTS; ++r) read(next, 0, r);
@@ -633,6 +651,16 @@ struct RowJobs {
                 clear<EB, TI, TJ, NT>(*job, a.parts > 1);
                 continue;
             }
+            // Weights whose lines are whole 2 KiB lie in few of the memory's channels at one
+            // place of the depth: neighbours begin at different steps (64 experts of 2 rows,
+            // 2048 x 2048 weights 123 us from the first step, 91 so; 40 rows 131 and 115).  Not
+            // where lines are of other widths (60 experts of 2 rows, 771 x 1001 weights 23.2 us,
+            // 24.9 so), where they read the same lines of many rows (8192^3 787 and 794 us), nor
+            // where the neighbours' weights are the rest of the same lines (drows of the 2 rows
+            // 125 and 130).
+            if (KIND == PRODUCT_FORWARD && TI < 256 && a.hidden * EB % 2048 == 0)
+                job->turn = tj % ((job->depth + STEP / EB - 1) / (STEP / EB));
+            else job->turn = 0;
             id += gridDim.x;
             return true;
         }
@@ -681,6 +709,7 @@ struct WeightJobs {
                 clear<EB, TI, TJ, NT>(*job, a.parts > 1);
                 continue;
             }
+            job->turn = 0;
             id += gridDim.x;
             return true;
         }
@@ -698,6 +727,10 @@ struct Shape {
 using Large = Shape<256, 256, 2, 4, 128, 1>;
 using Middle = Shape<128, 128, 2, 2, 128, 2>;
 using Small = Shape<32, 64, 1, 4, 256, 2>;
+// (drows of few rows reads 256 bytes of each line of weights, not 128: 64 experts of 2 rows,
+// 2048 x 2048 weights 126 us by Small, 96 so; but for few tiles, 4 experts of 50 rows,
+// 4096 x 4096 weights 27 us by Small, 40 so)
+using Flat = Shape<32, 128, 1, 4, 128, 2>;
 
 template <int EB, ProductKind KIND, bool AS, bool BS, class SHAPE>
 __global__ __launch_bounds__(SHAPE::NT, SHAPE::EACH * SHAPE::NT / 256) void k_product(
@@ -796,13 +829,17 @@ struct Cost {
     double each, step, alone;
 };
 // (measured on MI355X; see the table at the top)
-constexpr Cost kCosts[2][2][3] = {
+constexpr Cost kCosts[2][2][4] = {
     // bf16, lines for Straight; and through registers
-    {{{256, 256, 128, 1, 6.0, 1.4, 1.4}, {128, 128, 128, 2, 4.0, 1.0, 0.62}, {32, 64, 256, 2, 3.5, 0.62, 0.6}},
-     {{256, 256, 128, 1, 6.0, 9.0, 9.0}, {128, 128, 128, 2, 4.0, 1.5, 1.0}, {32, 64, 256, 2, 3.5, 1.0, 0.9}}},
+    {{{256, 256, 128, 1, 6.0, 1.4, 1.4}, {128, 128, 128, 2, 4.0, 1.0, 0.62}, {32, 64, 256, 2, 3.5, 0.62, 0.6},
+      {32, 128, 128, 2, 3.5, 0.5, 0.3}},
+     {{256, 256, 128, 1, 6.0, 9.0, 9.0}, {128, 128, 128, 2, 4.0, 1.5, 1.0}, {32, 64, 256, 2, 3.5, 1.0, 0.9},
+      {32, 128, 128, 2, 3.5, 0.6, 0.45}}},
     // fp32
-    {{{256, 256, 128, 1, 6.0, 99.0, 99.0}, {128, 128, 128, 2, 4.0, 3.7, 1.95}, {32, 64, 256, 2, 3.5, 1.13, 0.7}},
-     {{256, 256, 128, 1, 6.0, 99.0, 99.0}, {128, 128, 128, 2, 4.0, 3.7, 1.95}, {32, 64, 256, 2, 3.5, 1.13, 0.7}}}};
+    {{{256, 256, 128, 1, 6.0, 99.0, 99.0}, {128, 128, 128, 2, 4.0, 3.7, 1.95}, {32, 64, 256, 2, 3.5, 1.13, 0.7},
+      {32, 128, 128, 2, 3.5, 1.18, 0.76}},
+     {{256, 256, 128, 1, 6.0, 99.0, 99.0}, {128, 128, 128, 2, 4.0, 3.7, 1.95}, {32, 64, 256, 2, 3.5, 1.13, 0.7},
+      {32, 128, 128, 2, 3.5, 1.18, 0.76}}}};
 
 struct Plan {
     int shape;
@@ -819,7 +856,7 @@ Plan plan_of(ProductKind kind, size_t nrows, int experts, size_t hidden, size_t 
     const bool odd = eb == 2 && (hidden % 2 || (kind != PRODUCT_FORWARD && out % 2));
     Plan best{1, 1};
     double least = 1e300;
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < (kind == PRODUCT_DROWS ? 4 : 3); ++i) {
         const Cost& c = kCosts[eb == 4][odd][i];
         const size_t down = kind == PRODUCT_DWEIGHTS ? (out + c.ti - 1) / c.ti * (size_t)experts
                                                      : (rows + c.ti - 1) / c.ti * used;
@@ -849,6 +886,8 @@ hipError_t launch(const ProductArgs& a, hipStream_t s) {
     static_cast<ProductArgs&>(p) = a;
     p.parts = plan.parts;
     if (plan.shape == 2) return by_lines<EB, KIND, Small>(p, s);
+    if constexpr (KIND == PRODUCT_DROWS)
+        if (plan.shape == 3) return by_lines<EB, KIND, Flat>(p, s);
     if constexpr (EB == 2)
         if (plan.shape == 0) return by_lines<EB, KIND, Large>(p, s);
     return by_lines<EB, KIND, Middle>(p, s);
