@@ -16,6 +16,10 @@
 //      have a large share of it) are summed a piece of sorted places at a time.
 //   3. rows: the sum of each run, at the lanes of its first place, or of its
 //      pieces.
+// Measured: 16384 tokens of 4096 bf16 forward 33 us (84 MiB read and 128 written,
+// 6.7 TB/s: frequent tokens' rows come from the caches); their gradient into a table of
+// 131072 x 4096 247 us: order and clearing 162 - 177 us (1 GiB, 6.4 TB/s), pieces
+// 16, rows 52.  One token forward is the launch, 2.2 us of kernel.
 #include "model_ops.h"
 #include "ops_device.h"
 
@@ -513,8 +517,8 @@ unsigned blocks_for(size_t n, size_t each) {
 // The scratch: the sorted tokens, and past kWhole of them the buckets' counts,
 // begins and list; then the partial sums, where an id can have more tokens than a
 // piece.  Pieces are short while there are few tokens, so that a frequent one's
-// sum is spread over the card (16384 tokens of 4096, a piece of 16: 289 -> 245 us
-// against 64), and long where the partial sums would take much memory.
+// sum is spread over the card (16384 tokens of 4096: 247 us with a piece of 16,
+// 289 with 64), and long where the partial sums would take much memory.
 struct Layout {
     size_t order, start, length, live, count, begins, list, part, bytes;   // bytes from the start
     size_t pitch;                                           // floats of a partial row

@@ -20,9 +20,12 @@
 //   da = dacts u' s (1 + a' (1 - s)),  du = dacts a' s,  acts' = a' s u'
 // the last for the gradient of the weights that the activations met.
 //
-// All of it is bound by memory.  A thread has 8 values in a row, so a group is 4
-// neighbouring lanes and its maximum two DPP steps; the halves' units at the
-// same column belong to one thread.
+// All of it is bound by memory: the bytes of h, acts, codes and scales once, and a
+// dozen operations a value beside them.  A thread has 8 values in a row, so a
+// group is 4 neighbouring lanes and its maximum two DPP steps; the halves' units
+// at the same column belong to one thread.  Measured at 65536 x 2048 bf16: gate
+// 175 - 182 us (1.05 GB moved, 5.9 TB/s), gradient 223 us (1.35 GB, 6.0 TB/s),
+// values of the checkpoint read back 138 - 151 us (0.82 GB, 5.7 TB/s).
 #include "model_ops.h"
 #include "ops_device.h"
 
@@ -51,6 +54,9 @@ __device__ __forceinline__ void ld8(const char* row, size_t i, size_t n, float (
         }
     }
 }
+// (bf16 past the caches; fp32 through them, which join the two halves of a thread's 32
+// bytes: the gate's gradient of 65536 x 2048 fp32 488 us, 835 past them, values read back
+// 242 and 509)
 template <int EB>
 __device__ __forceinline__ void st8(char* row, size_t i, size_t n, const float (&v)[kV]) {
     if constexpr (EB == 2) {
@@ -59,7 +65,7 @@ __device__ __forceinline__ void st8(char* row, size_t i, size_t n, const float (
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float q[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-            st_unit_of<4, true>(row, i + 4 * h, n, Vec<4>::pack(q));
+            st_unit_of<4>(row, i + 4 * h, n, Vec<4>::pack(q));
         }
     }
 }

@@ -1,5 +1,26 @@
 // product.hip -- the experts' matrix products over ragged groups of rows, and
-// their gradients.
+// their gradients.  Expert e has the rows [offsets[e], offsets[e + 1]):
+//
+//   forward    y[j] = W_e x[j]               W_e is (out, hidden), out's rows contiguous
+//   drows      dx[j] = W_e^T dy[j]
+//   dweights   dW_e = sum over its rows j of dy[j] x[j]^T
+//
+// Each is C = A B^T for an operand of lines along the reduced dimension or across
+// it; the second kind is turned on the way from LDS into the matrix instructions
+// (bf16 by the transposing read, fp32 element by element), so nothing is
+// transposed in memory.  Sums are fp32 in the matrix accumulators and rounded
+// once, at the store.
+//
+// Blocks stay and walk the tiles of all experts, so that a group's last, partly
+// filled tile is next to others' work; the experts' tiles are counted on the
+// device from the offsets.  Many rows: bound by the matrix units and, at full
+// rate, by power (8192^3 bf16 forward 787 us, 1397 TFLOP/s; the three of 64
+// experts of 1024 rows, 4096 -> 2048, 910, 952 and 1066 us, 1208 to 1031 TFLOP/s,
+// the rest being the groups' part tiles and stores of tiles that end together).
+// Few rows: bound by reading the weights once (64 experts of 2 rows, 2048 -> 2048,
+// 537 MB in 91 us forward, 5.9 TB/s, and 96 us for drows); one row of 26 experts out of
+// the last-level cache 34 us.  Why there are several tiles, and in which order the depth is
+// walked, stands at Shape, at kCosts and at RowJobs.
 #include "model_ops.h"
 #include "ops_device.h"
 
@@ -828,7 +849,10 @@ struct Cost {
     int ti, tj, step_bytes, blocks;
     double each, step, alone;
 };
-// (measured on MI355X; see the table at the top)
+// (fitted on MI355X to times of each shape alone, between 1 tile and 8 a compute unit
+// and between 8 and 128 steps, weights in the last-level cache where they fit.  The
+// shapes' sides: 64 experts of 40 rows, 2048 -> 2048, drows 104 us in 128 x 128, 166 in
+// 32 x 64; 4 experts of 50 rows, 4096 -> 4096, 45 and 27)
 constexpr Cost kCosts[2][2][4] = {
     // bf16, lines for Straight; and through registers
     {{{256, 256, 128, 1, 6.0, 1.4, 1.4}, {128, 128, 128, 2, 4.0, 1.0, 0.62}, {32, 64, 256, 2, 3.5, 0.62, 0.6},
