@@ -622,9 +622,12 @@ struct Groups {
 };
 
 // The arguments, and how many parts the reduced dimension has: more than one
-// leave sums in 32 bits to `work`, one result after the other.
+// leave sums in 32 bits to `work`, one result after the other.  turned: whether
+// tiles may begin inside their depth (RowJobs), by the sizes alone, so that
+// the order of a sum does not depend on where the operands lie.
 struct PartArgs : ProductArgs {
     unsigned parts;
+    bool turned;
 };
 
 // The tiles of the rows' products (KIND: forward or drows) that this block has.
@@ -679,7 +682,7 @@ struct RowJobs {
             // 24.9 so), where they read the same lines of many rows (8192^3 787 and 794 us), nor
             // where the neighbours' weights are the rest of the same lines (drows of the 2 rows
             // 125 and 130).
-            if (KIND == PRODUCT_FORWARD && TI < 256 && a.hidden * EB % 2048 == 0)
+            if (KIND == PRODUCT_FORWARD && a.turned)
                 job->turn = tj % ((job->depth + STEP / EB - 1) / (STEP / EB));
             else job->turn = 0;
             id += gridDim.x;
@@ -909,6 +912,7 @@ hipError_t launch(const ProductArgs& a, hipStream_t s) {
     PartArgs p;
     static_cast<ProductArgs&>(p) = a;
     p.parts = plan.parts;
+    p.turned = plan.shape != 0 && a.hidden * EB % 2048 == 0;
     if (plan.shape == 2) return by_lines<EB, KIND, Small>(p, s);
     if constexpr (KIND == PRODUCT_DROWS)
         if (plan.shape == 3) return by_lines<EB, KIND, Flat>(p, s);

@@ -53,7 +53,7 @@ def test_embedding_between_guards(ctx, tokens, vocab, hidden, ib, t):  # noqa: F
 @pytest.mark.parametrize("t", [BF, F32])
 @pytest.mark.parametrize("counts,hidden,out", [
     ((1,), 1, 1), ((0, 3, 1, 0), 4104, 24), ((1, 0, 1, 1), 2048, 520), ((70, 0, 131), 776, 264),
-    ((70, 0, 131), 777, 265), ((129, 130), 640, 771), ((1100, 900), 520, 1032),
+    ((70, 0, 131), 777, 265), ((129, 130), 640, 771), ((1100, 900), 520, 1032), ((1100, 900), 1024, 1032),
     ((1100, 900), 521, 1031), ((40,), 8200, 40), ((2500,), 72, 48)])
 def test_products_between_guards(ctx, counts, hidden, out, t):  # noqa: F811
     lib = _lib.lib

@@ -74,6 +74,14 @@ def test_narrow(hidden, out, t):
     check((200, 0, 131, 1), hidden, out, t, 2)
 
 
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("counts,hidden,out", [((3, 0, 40), 8192, 200), ((130, 7), 1024, 600),
+                                               ((1, 1, 1, 0, 2), 2048, 1400), ((5,), 16384, 70)])
+def test_lines_a_power_of_two_apart(counts, hidden, out, t):
+    """Tiles that begin inside their depth, with the depth in parts and not."""
+    check(counts, hidden, out, t, 1)
+
+
 def test_large():
     """Tiles of every kind among many rows."""
     check((3000, 100, 0, 2500, 260, 1), 1024, 1280, BF, 30)
