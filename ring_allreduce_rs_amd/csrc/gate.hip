@@ -54,13 +54,13 @@ __device__ __forceinline__ void ld8(const char* row, size_t i, size_t n, float (
         }
     }
 }
-// (bf16 past the caches; fp32 through them, which join the two halves of a thread's 32
-// bytes: the gate's gradient of 65536 x 2048 fp32 488 us, 835 past them, values read back
-// 242 and 509)
-template <int EB>
+// (bf16 past the caches, unless NT is false; fp32 through them, which join the two halves
+// of a thread's 32 bytes: the gate's gradient of 65536 x 2048 fp32 488 us, 835 past them,
+// values read back 242 and 509)
+template <int EB, bool NT = true>
 __device__ __forceinline__ void st8(char* row, size_t i, size_t n, const float (&v)[kV]) {
     if constexpr (EB == 2) {
-        st_unit_of<2, true>(row, i, n, Vec<2>::pack(v));
+        st_unit_of<2, NT>(row, i, n, Vec<2>::pack(v));
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void k_restore(const GateArgs a, unsigned
     }
 }
 
-template <int EB>
+template <int EB, bool NT>
 __global__ __launch_bounds__(kThreads) void k_gate(const GateArgs a, unsigned units, size_t blocks) {
     const size_t groups = units / kLanes;
     for (size_t b = blockIdx.x; b < blocks; b += gridDim.x) {
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void k_gate(const GateArgs a, unsigned un
         }
 #pragma unroll
         for (int j = 0; j < kV; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j];
-        st8<EB>(static_cast<char*>(a.y) + s.row * a.cols * EB, s.col, a.cols, g);
+        st8<EB, NT>(static_cast<char*>(a.y) + s.row * a.cols * EB, s.col, a.cols, g);
     }
 }
 
@@ -255,20 +255,27 @@ constexpr size_t kMostBlocks = size_t(1) << 22;
 
 }  // namespace
 
-#define LAUNCH(KERNEL)                                                                            \
+#define LAUNCH(KERNEL) LAUNCH_AS(KERNEL<2>, KERNEL<4>)
+#define LAUNCH_AS(TWO, FOUR)                                                                      \
     do {                                                                                          \
         if (a.rows == 0) return hipSuccess;                                                       \
         const unsigned units = units_of(a.cols);                                                  \
         const size_t blocks = (a.rows * units + kThreads - 1) / kThreads;                         \
         const dim3 grid((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks));                 \
-        if (a.eb == 2) hipLaunchKernelGGL(KERNEL<2>, grid, dim3(kThreads), 0, s, a, units, blocks); \
-        else hipLaunchKernelGGL(KERNEL<4>, grid, dim3(kThreads), 0, s, a, units, blocks);         \
+        if (a.eb == 2) hipLaunchKernelGGL((TWO), grid, dim3(kThreads), 0, s, a, units, blocks);   \
+        else hipLaunchKernelGGL((FOUR), grid, dim3(kThreads), 0, s, a, units, blocks);            \
         return hipGetLastError();                                                                 \
     } while (0)
 
 hipError_t launch_save(const GateArgs& a, hipStream_t s) { LAUNCH(k_save); }
 hipError_t launch_restore(const GateArgs& a, hipStream_t s) { LAUNCH(k_restore); }
-hipError_t launch_gate(const GateArgs& a, hipStream_t s) { LAUNCH(k_gate); }
+// Activations go past the caches, except in rows that share their ends' lines (bf16, past
+// and through them: 65536 x 1001 119 and 97 us; 2000 x 4096 13.1 and 14.4, 8192 x 2048 24.9
+// and 26.2; 65536 x 2048 179 and 166 alone, 322 and 324 with the checkpoint read back).
+hipError_t launch_gate(const GateArgs& a, hipStream_t s) {
+    if (a.cols % 8 == 0) LAUNCH_AS((k_gate<2, true>), (k_gate<4, true>));
+    else LAUNCH_AS((k_gate<2, false>), (k_gate<4, true>));
+}
 hipError_t launch_gate_grad(const GateArgs& a, hipStream_t s) { LAUNCH(k_gate_grad); }
 
 }  // namespace arlib
