@@ -617,6 +617,17 @@ const int* plan_offsets(PyObject* o, const at::Tensor& like, int64_t* experts) {
     return static_cast<const int*>(dense(t, "plan.offsets", at::kInt, t.sizes(), like));
 }
 
+// The rows of a product are those of the plan's dispatch, as many as it has slots.
+void plan_rows(PyObject* o, const at::Tensor& rows, const char* name) {
+    const at::Tensor& t = tensor(o, "plan.dest");
+    if (t.dim() != 2 || t.size(1) == 0)
+        throw Refused("plan.dest has shape " + shape_of(t) + ", needs (tokens, topk)");
+    dense(t, "plan.dest", at::kInt, t.sizes(), rows);
+    if (rows.size(0) != t.numel())
+        throw Refused(std::string(name) + " has shape " + shape_of(rows) + ", needs the plan's " +
+                      std::to_string(t.numel()) + " rows");
+}
+
 size_t product_workspace(ar_expert_product p, int64_t rows, int64_t experts, int64_t hidden,
                          int64_t out, ar_dtype dt) {
     size_t bytes = 0;
@@ -628,7 +639,7 @@ size_t product_workspace(ar_expert_product p, int64_t rows, int64_t experts, int
 // ar_expert_matmul (KIND AR_EXPERT_FORWARD) or ar_expert_matmul_drows
 template <ar_expert_product KIND>
 PyObject* product_of_rows(PyObject* const* args, Py_ssize_t n, const char* name) {
-    return guarded(n, 3, [&]() -> PyObject* {
+    return guarded(n, 4, [&]() -> PyObject* {
         constexpr bool kForward = KIND == AR_EXPERT_FORWARD;
         const Rows r(args[0], name);
         const at::Tensor& w = tensor(args[1], "weights");
@@ -640,10 +651,11 @@ PyObject* product_of_rows(PyObject* const* args, Py_ssize_t n, const char* name)
             throw Refused(std::string(name) + " " + shape_of(r.t) + " does not match weights " +
                           shape_of(w));
         int64_t experts;
-        const int* offsets = plan_offsets(args[2], r.t, &experts);
+        const int* offsets = plan_offsets(args[3], r.t, &experts);
         if (experts != w.size(0))
             throw Refused("weights " + shape_of(w) + " are not of the plan's " +
                           std::to_string(experts) + " experts");
+        plan_rows(args[2], r.t, name);
         at::Tensor y = make({rows, kForward ? out : hidden}, r.t.scalar_type(), r.t);
         const Scratch ws(product_workspace(KIND, rows, experts, hidden, out, r.dt), r.t);
         ar_ctx* c = context(r.t.get_device());
@@ -664,13 +676,14 @@ PyObject* expert_matmul_drows(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 PyObject* expert_matmul_dweights(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    return guarded(n, 3, [&]() -> PyObject* {
+    return guarded(n, 4, [&]() -> PyObject* {
         const Rows d(args[0], "dout"), r(args[1], "rows");
         if (d.dt != r.dt || d.t.size(0) != r.t.size(0) || d.t.device() != r.t.device())
             throw Refused("dout " + shape_of(d.t) + " does not match rows " + shape_of(r.t) +
                           " in dtype, rows or device");
         int64_t experts;
-        const int* offsets = plan_offsets(args[2], r.t, &experts);
+        const int* offsets = plan_offsets(args[3], r.t, &experts);
+        plan_rows(args[2], r.t, "rows");
         const int64_t rows = r.t.size(0), hidden = r.t.size(1), out = d.t.size(1);
         const size_t bytes = product_workspace(AR_EXPERT_DWEIGHTS, rows, experts, hidden, out, r.dt);
         at::Tensor dw = make({experts, out, hidden}, r.t.scalar_type(), r.t);

@@ -132,19 +132,20 @@ def embedding_backward(dy, ids, vocab: int, scale: float = 1.0):
 def expert_matmul(rows, weights, plan: ExpertPlan):
     """Each expert's product with its own rows of a dispatch: rows (n, hidden) and
     weights (experts, out, hidden) give (n, out), out[j] = rows[j] @
-    weights[e].T for the rows j of expert e; zeros in the rows without one."""
-    return _ops.expert_matmul(rows, weights, plan[2])
+    weights[e].T for the rows j of expert e; zeros in the rows without one.  As
+    many rows as the plan has slots, here and in the gradients."""
+    return _ops.expert_matmul(rows, weights, plan[0], plan[2])
 
 
 def expert_matmul_drows(dout, weights, plan: ExpertPlan):
     """Gradient of ``expert_matmul``'s rows: dout[j] @ weights[e]."""
-    return _ops.expert_matmul_drows(dout, weights, plan[2])
+    return _ops.expert_matmul_drows(dout, weights, plan[0], plan[2])
 
 
 def expert_matmul_dweights(dout, rows, plan: ExpertPlan):
     """Gradient of ``expert_matmul``'s weights, of the rows' dtype: for each expert
     dout[j].T @ rows[j] over its rows, zeros without any."""
-    return _ops.expert_matmul_dweights(dout, rows, plan[2])
+    return _ops.expert_matmul_dweights(dout, rows, plan[0], plan[2])
 
 
 class Saved8(NamedTuple):
