@@ -240,7 +240,10 @@ __global__ __launch_bounds__(kThreads) void k_gate_grad(const GateArgs a, unsign
         for (int j = 0; j < kV; ++j) {
             const float q = sigmoid(g[j]), gq = g[j] * q;
             du[j] = d[j] * gq;
-            da[j] = d[j] * u[j] * q * (1.0f + g[j] * (1.0f - q));
+            // (q f, f = 1 + a (1 - s), is 1.1 at most, and comes before the factors that may be
+            // as large as the type's lowest value in masked places; half of it, as 1.1 times
+            // these is past the numbers, where the whole product may not be)
+            da[j] = 2.0f * (d[j] * (u[j] * (q * (0.5f * (1.0f + g[j] * (1.0f - q))))));
             g[j] = gq * u[j];
         }
         char* dh = static_cast<char*>(a.y) + at * a.cols * EB;
