@@ -132,18 +132,32 @@ __device__ __forceinline__ void decode(codes_reg c, int b, float (&v)[kV]) {
         v[j] = (float)(int8_t)(c[j / 4] >> (8 * (j % 4))) * scale;
 }
 
-// 1 / (1 + e^-a).  The product a log2(e) is kept to more than 32 bits, so that
-// e^-a is good to 2 ulp where it is large; past fp32's range it is 0 or
-// infinite, and the sigmoid 1 or 0.
+// 1 / (1 + e^-a) for |a| < 64.  The product a log2(e) is kept to more than 32 bits, so that
+// e^-a is good to 2 ulp where it is large.
 __device__ __forceinline__ float sigmoid(float a) {
-    // (an infinite a would make NaN of the rest; NaN itself comes in by a's other factors)
-    a = __builtin_amdgcn_fmed3f(a, -128.0f, 128.0f);
     const float hi = a * -kLog2e;
     float e = __builtin_amdgcn_exp2f(hi);
     const float lo = __builtin_fmaf(a, -kLog2e, -hi) - a * kLog2eLow;
     e *= __builtin_fmaf(lo, kLn2, 1.0f);
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
+// For any a, as e^a / (1 + e^a) where a < 0: it may lie below fp32's normal numbers and yet
+// have ordinary products with a large u or dacts, so it and they are in 64 bits.  0 below -400,
+// where no product of three fp32 numbers is one.
+__device__ __forceinline__ double far_sigmoid(float a) {
+    // (an infinite a would make NaN of the rest; NaN itself comes in by a's other factors)
+    const float x = __builtin_amdgcn_fmed3f(__builtin_fabsf(a), 0.0f, 400.0f);
+    const float hi = x * -kLog2e, n = __builtin_rintf(hi);
+    const float lo = __builtin_fmaf(x, -kLog2e, -hi) - x * kLog2eLow;
+    const float e = __builtin_amdgcn_exp2f(hi - n) * __builtin_fmaf(lo, kLn2, 1.0f);
+    const double z = x < 400.0f ? __builtin_ldexp((double)e, (int)n) : 0.0;   // e^-|a|
+    const double r = __builtin_amdgcn_rcpf(1.0f + (float)z);
+    return a < 0.0f ? z * r : r;
+}
+// The scale's exponent from which on a group may hold magnitudes of 64 and more.  (65536 x
+// 2048 bf16, gate and gradient: no such group 180 and 218 us, all of them 193 and 223, as
+// before; lanes of both kinds in each wavefront 215 and 248)
+constexpr int kFar = 127;
 
 // Where a block's thread works: its row and column.  The units of all rows lie
 // in one line, each row padded to whole groups.
@@ -214,14 +228,20 @@ __global__ __launch_bounds__(kThreads) void k_gate(const GateArgs a, unsigned un
             a.scales[at * groups + s.col / kSaveGroup] = (uint8_t)eg;
             a.scales[(at + 1) * groups + s.col / kSaveGroup] = (uint8_t)eu;
         }
+        if (__builtin_expect(eg < kFar, 1)) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j];
+            for (int j = 0; j < kV; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kV; ++j)
+                g[j] = (float)((double)g[j] * far_sigmoid(g[j]) * (double)u[j]);
+        }
         st8<EB, NT>(static_cast<char*>(a.y) + s.row * a.cols * EB, s.col, a.cols, g);
     }
 }
 
 template <int EB>
-__global__ __launch_bounds__(kThreads) void k_gate_grad(const GateArgs a, unsigned units,
+__global__ __launch_bounds__(kThreads, 8) void k_gate_grad(const GateArgs a, unsigned units,
                                                         size_t blocks) {
     const size_t groups = units / kLanes;
     for (size_t b = blockIdx.x; b < blocks; b += gridDim.x) {
@@ -236,15 +256,27 @@ __global__ __launch_bounds__(kThreads) void k_gate_grad(const GateArgs a, unsign
         decode(cg, eg, g);
         decode(cu, eu, u);
         float da[kV], du[kV];
+        if (__builtin_expect(eg < kFar, 1)) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const float q = sigmoid(g[j]), gq = g[j] * q;
-            du[j] = d[j] * gq;
-            // (q f, f = 1 + a (1 - s), is 1.1 at most, and comes before the factors that may be
-            // as large as the type's lowest value in masked places; half of it, as 1.1 times
-            // these is past the numbers, where the whole product may not be)
-            da[j] = 2.0f * (d[j] * (u[j] * (q * (0.5f * (1.0f + g[j] * (1.0f - q))))));
-            g[j] = gq * u[j];
+            for (int j = 0; j < kV; ++j) {
+                const float q = sigmoid(g[j]), gq = g[j] * q;
+                du[j] = d[j] * gq;
+                // (q f, f = 1 + a (1 - s), is 1.1 at most, and comes before the factors that may
+                // be as large as the type's lowest value in masked places; half of it, as 1.1
+                // times these is past the numbers, where the whole product may not be)
+                da[j] = 2.0f * (d[j] * (u[j] * (q * (0.5f * (1.0f + g[j] * (1.0f - q))))));
+                g[j] = gq * u[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kV; ++j) {
+                settle(g[j]), settle(u[j]), settle(d[j]);   // (one value after another: few registers)
+                const double q = far_sigmoid(g[j]), gq = (double)g[j] * q, v = u[j], x = d[j];
+                du[j] = (float)(x * gq);
+                da[j] = (float)(x * v * (q * (1.0 + (double)g[j] * (1.0 - q))));
+                g[j] = (float)(gq * v);
+                settle(du[j]), settle(da[j]), settle(g[j]);
+            }
         }
         char* dh = static_cast<char*>(a.y) + at * a.cols * EB;
         st8<EB>(dh, s.col, a.cols, da);
