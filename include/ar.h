@@ -624,9 +624,9 @@ ar_status ar_expert_matmul_workspace(ar_expert_product product, size_t nrows, in
  * 2^(scale - 127) >= the group's largest magnitude, and code is the value over
  * it to the nearest, ties to even (from -63 to 63 where the scale is 2^122, so
  * that no value read back is infinite).  A group with an infinity or a NaN has
- * scale 255 and codes 0, and reads back as NaN.  Values read back are exact in
- * bfloat16 and binary32.  cols > 0 and <= 2^28 (AR_ERR_UNSUPPORTED); rows == 0
- * is a successful no-op.
+ * scale 255 and codes 0, and reads back as NaN; scale 0 is no checkpoint's, and
+ * reads back as 0.  Values read back are exact in bfloat16 and binary32.
+ * cols > 0 and <= 2^28 (AR_ERR_UNSUPPORTED); rows == 0 is a successful no-op.
  * codes: rows x cols; scales: rows x ceil(cols / AR_SAVE_GROUP). */
 #define AR_SAVE_GROUP 32
 ar_status ar_save_8bit(ar_ctx* ctx, const void* x, size_t x_stride, size_t rows, size_t cols,

@@ -6,9 +6,9 @@
 // shorter).  With m the group's largest magnitude, the scale is the least
 // 2^(b - 127), b >= 1, with m <= 127 * 2^(b - 127): read off m's bits, so that
 // scale, codes and the values read back are exact and the same everywhere.  A
-// value is off by at most half a scale, m / 127 at most (by a whole one where m
-// is above 1.984375 * 2^127 and codes end at 63, so that values read back stay
-// finite).  The values have 7 significant bits, so reading them back as bf16
+// value is off by at most half a scale: by max(m / 127, 2^-127), as no scale is
+// below 2^-126.  Where m is above 1.984375 * 2^127, codes end at 63, so that
+// values read back stay finite, and a value is off by less than the scale, 2^122.  The values have 7 significant bits, so reading them back as bf16
 // rounds nothing.  A group that
 // holds an infinity or a NaN has b = 255 and codes 0, and reads back as NaN
 // (0 * 2^128 as binary32 computes it).

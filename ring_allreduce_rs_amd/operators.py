@@ -162,7 +162,9 @@ class Saved8(NamedTuple):
 def save_8bit(x):
     """x in 8 bits, groups of 32 along the last dimension sharing a power of two as
     their scale: each value is off by half a scale at most, which is no more
-    than the group's largest magnitude over 127."""
+    than the group's largest magnitude m over 127, or 2**-127 where that is more
+    (a magnitude below it reads back as 0).  Where m is above 1.984375 * 2**127,
+    codes end at 63 and a value is off by less than a whole scale, 2**122."""
     return Saved8(*_ops.save_8bit(x))
 
 
