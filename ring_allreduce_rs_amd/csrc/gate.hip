@@ -158,6 +158,8 @@ __device__ __forceinline__ double far_sigmoid(float a) {
 // 2048 bf16, gate and gradient: no such group 180 and 218 us, all of them 193 and 223, as
 // before; lanes of both kinds in each wavefront 215 and 248)
 constexpr int kFar = 127;
+// That from which on 1.1 times a magnitude may be past the numbers.
+constexpr int kVast = 248;
 
 // Where a block's thread works: its row and column.  The units of all rows lie
 // in one line, each row padded to whole groups.
@@ -256,15 +258,15 @@ __global__ __launch_bounds__(kThreads, 8) void k_gate_grad(const GateArgs a, uns
         decode(cg, eg, g);
         decode(cu, eu, u);
         float da[kV], du[kV];
-        if (__builtin_expect(eg < kFar, 1)) {
+        if (__builtin_expect(eg < kFar && eu < kVast, 1)) {
 #pragma unroll
             for (int j = 0; j < kV; ++j) {
                 const float q = sigmoid(g[j]), gq = g[j] * q;
                 du[j] = d[j] * gq;
-                // (q f, f = 1 + a (1 - s), is 1.1 at most, and comes before the factors that may
-                // be as large as the type's lowest value in masked places; half of it, as 1.1
-                // times these is past the numbers, where the whole product may not be)
-                da[j] = 2.0f * (d[j] * (u[j] * (q * (0.5f * (1.0f + g[j] * (1.0f - q))))));
+                // (s f, f = 1 + a (1 - s), is 1.1 at most, and comes before the factors that are
+                // as large as the type's lowest value in masked places: dacts u may be infinite
+                // where the gradient is not)
+                da[j] = d[j] * (u[j] * (q * (1.0f + g[j] * (1.0f - q))));
                 g[j] = gq * u[j];
             }
         } else {

@@ -16,8 +16,8 @@ def test_gradient_at_the_lowest_value(t):
     low = torch.finfo(t).min
     a = torch.tensor([low, -1e30, -1e4, -200.0, -60.0, -50.0, -20.0, 0.0, 1.0, 2.0, 5.0, 1e4])
     d = torch.tensor([0.01, 0.8, 2.0, -4.0, 100.0, -1e4])
-    # a row, with groups of its own, for each a; u lowest or as large upwards
-    for top in (low, -low):
+    # a row, with groups of its own, for each a; u lowest, as large upwards, and half as large
+    for top in (low, -low, 1.6e38):
         h = torch.cat([a[:, None].expand(-1, 64), torch.full((12, 64), top)], 1).to(t).cuda()
         _, saved = ar.silu_gate(h)
         dacts = d.repeat(11)[:64].to(t).expand(12, 64).contiguous()
