@@ -13,10 +13,13 @@
 //
 // Blocks stay and walk the tiles of all experts, so that a group's last, partly
 // filled tile is next to others' work; the experts' tiles are counted on the
-// device from the offsets.  Many rows: bound by the matrix units and, at full
-// rate, by power (8192^3 bf16 forward 787 us, 1397 TFLOP/s; the three of 64
+// device from the offsets.  Many rows: bound by the matrix units at a clock of
+// 2.05 of 2.4 GHz (8192^3 bf16 forward 787 us, 1397 TFLOP/s; the three of 64
 // experts of 1024 rows, 4096 -> 2048, 910, 952 and 1066 us, 1208 to 1031 TFLOP/s,
-// the rest being the groups' part tiles and stores of tiles that end together).
+// the rest being stores of tiles that end together).  Ragged groups cost part
+// tiles and a last round of few (65536 rows in 290 tiles of 256: ten rounds, 1040
+// us) and, in the weights' gradient, dies with deeper tiles than others (131072
+// rows over 128 experts, 2048 x 1024: 634 - 660 us, equal groups 555).
 // Few rows: bound by reading the weights once (64 experts of 2 rows, 2048 -> 2048,
 // 537 MB in 91 us forward, 5.9 TB/s, and 96 us for drows); one row of 26 experts out of
 // the last-level cache 34 us.  Why there are several tiles, and in which order the depth is
