@@ -8,10 +8,10 @@
 // scale, codes and the values read back are exact and the same everywhere.  A
 // value is off by at most half a scale: by max(m / 127, 2^-127), as no scale is
 // below 2^-126.  Where m is above 1.984375 * 2^127, codes end at 63, so that
-// values read back stay finite, and a value is off by less than the scale, 2^122.  The values have 7 significant bits, so reading them back as bf16
-// rounds nothing.  A group that
-// holds an infinity or a NaN has b = 255 and codes 0, and reads back as NaN
-// (0 * 2^128 as binary32 computes it).
+// values read back stay finite, and a value is off by less than the scale, 2^122.
+// The values have 7 significant bits, so reading them back as bf16 rounds
+// nothing.  A group that holds an infinity or a NaN has b = 255 and codes 0, and
+// reads back as NaN (0 * 2^128 as binary32 computes it).
 //
 // The gate takes rows h = (a, u) of two halves of `cols` values:
 //   acts = a s u, s = sigmoid(a) = 1 / (1 + e^-a)
@@ -142,8 +142,8 @@ __device__ __forceinline__ float sigmoid(float a) {
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
 // For any a, as e^a / (1 + e^a) where a < 0: it may lie below fp32's normal numbers and yet
-// have ordinary products with a large u or dacts, so it and they are in 64 bits.  0 below -400,
-// where no product of three fp32 numbers is one.
+// have ordinary products with a large u and dacts, so it and they are in 64 bits.  0 below
+// -400, where the largest of them is below fp32's numbers.
 __device__ __forceinline__ double far_sigmoid(float a) {
     // (an infinite a would make NaN of the rest; NaN itself comes in by a's other factors)
     const float x = __builtin_amdgcn_fmed3f(__builtin_fabsf(a), 0.0f, 400.0f);
@@ -154,9 +154,9 @@ __device__ __forceinline__ double far_sigmoid(float a) {
     const double r = __builtin_amdgcn_rcpf(1.0f + (float)z);
     return a < 0.0f ? z * r : r;
 }
-// The scale's exponent from which on a group may hold magnitudes of 64 and more.  (65536 x
-// 2048 bf16, gate and gradient: no such group 180 and 218 us, all of them 193 and 223, as
-// before; lanes of both kinds in each wavefront 215 and 248)
+// The scale's exponent from which on a group may hold magnitudes of 64 and more, and 32 bits do
+// not.  (65536 x 2048 bf16, gate and gradient: no such group 180 and 218 us, all of them 193
+// and 223, lanes of both kinds in each wavefront 215 and 248)
 constexpr int kFar = 127;
 // That from which on 1.1 times a magnitude may be past the numbers.
 constexpr int kVast = 248;
@@ -242,9 +242,10 @@ __global__ __launch_bounds__(kThreads) void k_gate(const GateArgs a, unsigned un
     }
 }
 
+// (64 registers at most, for 8 wavefronts a SIMD)
 template <int EB>
 __global__ __launch_bounds__(kThreads, 8) void k_gate_grad(const GateArgs a, unsigned units,
-                                                        size_t blocks) {
+                                                           size_t blocks) {
     const size_t groups = units / kLanes;
     for (size_t b = blockIdx.x; b < blocks; b += gridDim.x) {
         const Spot s = spot(b, a.rows, units);
